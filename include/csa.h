@@ -92,6 +92,8 @@ typedef struct csa_fmt {
 #define CSA_OP_COMPRESS 4
 #define CSA_OP_OUT_PROJ 5   /* Tq = T, N = g * d_g */
 #define CSA_OP_INDEXER_MX 6 /* indexer_scores_topk_mxfp8 */
+#define CSA_OP_FP8_MATMUL 7 /* Tq = M */
+#define CSA_OP_OUT_PROJ_FP8 8 /* Tq = T, H, c, N = g * d_g */
 
 /* ---- (1) compression ------------------------------------------------ */
 
@@ -397,6 +399,88 @@ csa_status grouped_output_projection(int32_t dtype, int64_t T, int32_t H, int32_
                                      int32_t d_g, int32_t d, const void* o, const void* w_group,
                                      const void* w_out, void* y, void* ws, size_t ws_bytes,
                                      void* stream);
+
+/* ---- (5) the 8-bit projection path ------------------------------------- */
+
+/*
+ * FP8 matrices of the calls below: E4M3 codes (bytes), and one UE8M0 scale
+ * byte e + 127 per block of 128 columns -- of one row for activations
+ * (scales [rows, ceil(d/128)]), of 128 rows for weights (scales
+ * [ceil(rows/128), ceil(d/128)]); the last blocks may be short.  The value of
+ * code c is c 2^e.  Written here, e is the smallest integer >= -127 with
+ * amax <= 448 2^e, amax over the block's finite elements (scale byte 0 where
+ * there is none, or all are zero), and codes are rounded to nearest even: no
+ * finite element saturates.  NaN and infinity become the NaN code.  Scale
+ * byte 255 is NaN.  Codes and scales are contiguous, codes 16-byte aligned, d
+ * a multiple of 16 (else CSA_E_UNSUPPORTED).
+ * The summary page gives no format for the projections; power-of-two scales
+ * are what the block-scaled tensor cores apply, and a code of normal size has
+ * the same relative error under any scale.
+ */
+
+/*
+ * RMSNorm with the residual addition, in E4M3 [§3.3 of the summary page has
+ * RMSNorm before the attention's products; here it feeds the layer's
+ * projections]:
+ *   h = x + residual (x alone when residual is NULL), in float32;
+ *   y = h / sqrt(mean(h^2) + eps) * gain (gain NULL: 1), in float32;
+ *   codes, scales = y as FP8 activations; sum_out = h rounded to dtype.
+ *   x, residual: [T, d] (dtype), row strides x_ld, res_ld elements;
+ *   gain: [d] float32; sum_out: [T, d] (dtype), row stride sum_ld, or NULL; it
+ *   may be x or residual itself (same pointer and stride).  Row strides in
+ *   bytes are multiples of 16 and pointers 16-byte aligned.  The norm is taken
+ *   of the unrounded h.  A row whose sum of squares is beyond float32 is
+ *   scaled down first; a row with an infinity gives NaN there and 0 elsewhere.
+ * Errors: CSA_E_ARG (null or misaligned pointers, bad dtype, T < 0, d < 1, a
+ * stride below d, eps < 0 or NaN, sum_out without residual); CSA_E_UNSUPPORTED
+ * (d not a multiple of 16, or above 32768).
+ */
+csa_status rmsnorm_fp8(int32_t dtype, int64_t T, int32_t d, const void* x, int64_t x_ld,
+                       const void* residual, int64_t res_ld, const float* gain, float eps,
+                       void* sum_out, int64_t sum_ld, void* codes, void* scales, void* stream);
+
+/*
+ * x [rows, d] (dtype, row stride ld elements) as FP8 activations
+ * (block_rows = 1) or FP8 weights (block_rows = 128).  Errors: CSA_E_ARG (as
+ * rmsnorm_fp8, or block_rows neither 1 nor 128), CSA_E_UNSUPPORTED.
+ */
+csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, int64_t ld,
+                        int32_t block_rows, void* codes, void* scales, void* stream);
+
+/*
+ * y = x w^T of FP8 activations x [M, K] and FP8 weights w [N, K], products
+ * summed in float32 and rounded once to out_dtype (CSA_BF16 or CSA_F32).
+ *   y: [M, N], row stride y_ld elements (a column slice of a wider buffer is
+ *   fine; any alignment of its element type).
+ *   ws: >= csa_workspace_bytes(CSA_OP_FP8_MATMUL, ...) = 256 bytes (status
+ *   word), zeroed before first use.
+ * A row's result does not depend on the other rows' values; it may differ in
+ * its last bits between values of M, which choose the split of K.
+ * Errors: CSA_E_ARG (null or misaligned pointers, bad out_dtype, negative M or
+ * N, K < 1, y_ld < N), CSA_E_UNSUPPORTED (K not a multiple of 16, or M, N, K
+ * beyond 2^31 - 1), CSA_E_WORKSPACE.
+ */
+csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const void* x_codes,
+                      const void* x_scales, const void* w_codes, const void* w_scales, void* y,
+                      int64_t y_ld, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * grouped_output_projection in FP8: with Q(.) the FP8 activations of a row,
+ *   v[t, j d_g + n] = sum_k Q(o)[t, j (H/g) c + k] w_group[j, n, k]
+ *   y[t, n]         = sum_k Q(v)[t, k] w_out[n, k]
+ * v is quantized from its float32 sums.  o: [T, H, c] (CSA_BF16 or CSA_F32);
+ * w_group: [g, d_g, (H/g) c] codes, w_group_scales [g, d_g/128, (H/g) c/128];
+ * w_out: [d, g d_g] codes, w_out_scales [ceil(d/128), g d_g/128]; y (out):
+ * [T, d] bf16.  ws: >= csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dtype, 1, T,
+ * H, c, g d_g, 0, 0).
+ * Errors: CSA_E_ARG, CSA_E_WORKSPACE, and CSA_E_UNSUPPORTED unless H % g == 0
+ * and (H/g) c and d_g are multiples of 128.
+ */
+csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, int32_t c,
+                                         int32_t g, int32_t d_g, int32_t d, const void* o,
+                                         const void* w_group, const void* w_group_scales,
+                                         const void* w_out, const void* w_out_scales, void* y,
+                                         void* ws, size_t ws_bytes, void* stream);
 
 /* ---- workspace and status --------------------------------------------- */
 

@@ -6,6 +6,7 @@ names of the C entry points (include/csa.h):
 
     csa_compress, hca_compress, csa_compress_append, hca_compress_append,
     indexer_scores_topk, sparse_mqa_attn, dense_hca_attn, grouped_output_projection,
+    rmsnorm_fp8, fp8_quantize, fp8_matmul, grouped_output_projection_fp8,
     csa_workspace_bytes, csa_check_status
 
 Importing succeeds without a GPU; calling any op without the built library or
@@ -26,7 +27,7 @@ CSA_OK, CSA_E_ARG, CSA_E_UNSUPPORTED, CSA_E_CUDA, CSA_E_DEVICE, CSA_E_WORKSPACE 
 CSA_F32, CSA_BF16 = 0, 1
 CSA_F_NO_NORM, CSA_F_NO_ROPE, CSA_F_PORTABLE, CSA_F_MIXED = 1, 2, 4, 8
 (CSA_OP_INDEXER, CSA_OP_SPARSE_ATTN, CSA_OP_DENSE_ATTN, CSA_OP_COMPRESS, CSA_OP_OUT_PROJ,
- CSA_OP_INDEXER_MX) = 1, 2, 3, 4, 5, 6
+ CSA_OP_INDEXER_MX, CSA_OP_FP8_MATMUL, CSA_OP_OUT_PROJ_FP8) = 1, 2, 3, 4, 5, 6, 7, 8
 CSA_DEV_TIMEOUT, CSA_DEV_RANGE, CSA_DEV_BAD_INDEX, CSA_DEV_STREAM = 1, 2, 3, 4
 
 EXPORTED = (
@@ -35,7 +36,8 @@ EXPORTED = (
     "indexer_mxfp8_quantize", "indexer_scores_topk_mxfp8", "indexer_mxfp4_quantize",
     "indexer_scores_topk_mxfp4", "csa_mixed_record_bytes",
     "csa_store_mixed", "sparse_mqa_attn", "dense_hca_attn",
-    "grouped_output_projection", "csa_workspace_bytes",
+    "grouped_output_projection", "rmsnorm_fp8", "fp8_quantize", "fp8_matmul",
+    "grouped_output_projection_fp8", "csa_workspace_bytes",
     "csa_check_status",
     "csa_status_string", "csa_launch_count", "csa_selftest_wait",
 )
@@ -117,6 +119,11 @@ def lib():
                                             P, P, P, sz, P]
     L.grouped_output_projection.argtypes = [i32, i64, i32, i32, i32, i32, i32, P, P, P, P, P, sz,
                                             P]
+    L.rmsnorm_fp8.argtypes = [i32, i64, i32, P, i64, P, i64, P, f32, P, i64, P, P, P]
+    L.fp8_quantize.argtypes = [i32, i64, i32, P, i64, i32, P, P, P]
+    L.fp8_matmul.argtypes = [i32, i64, i64, i64, P, P, P, P, P, i64, P, sz, P]
+    L.grouped_output_projection_fp8.argtypes = [i32, i64, i32, i32, i32, i32, i32, P, P, P, P, P,
+                                                P, P, sz, P]
     L.csa_workspace_bytes.argtypes = [i32, i32, i64, i64, i32, i32, i64, i32, i32]
     L.csa_workspace_bytes.restype = sz
     L.csa_check_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_uint32)]
@@ -130,7 +137,8 @@ def lib():
                "indexer_scores_topk_noalloc", "sparse_mqa_attn", "dense_hca_attn",
                "grouped_output_projection", "indexer_mxfp8_quantize", "csa_store_mixed",
                "indexer_mxfp4_quantize", "indexer_scores_topk_mxfp4",
-               "indexer_scores_topk_mxfp8", "csa_check_status", "csa_selftest_wait"):
+               "indexer_scores_topk_mxfp8", "rmsnorm_fp8", "fp8_quantize", "fp8_matmul",
+               "grouped_output_projection_fp8", "csa_check_status", "csa_selftest_wait"):
         getattr(L, fn).restype = i32
     _lib = L
     return L
@@ -425,3 +433,170 @@ def grouped_output_projection(o, w_group, w_out, y=None, ws=None, stream=None):
     _check(st, "grouped_output_projection")
     return y
 
+
+
+def _launch(dev, stream, what, fn, *args):
+    """fn(*args, stream) on `dev`'s current stream unless one is given, with
+    `dev` current while it launches."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != CSA_OK:
+        raise CSAError(st, what)
+
+
+def _arg(ok, what: str):
+    if not ok:
+        raise CSAError(CSA_E_ARG, what)
+
+
+def _fp8(t, shape, dev, what: str):
+    """Address of contiguous FP8 codes or scales of the given shape on dev."""
+    _arg(t.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu), f"{what}: dtype")
+    _arg(tuple(t.shape) == shape, f"{what}: shape {tuple(t.shape)}, expected {shape}")
+    _arg(t.is_contiguous() and t.device == dev, f"{what}: contiguous, on {dev}")
+    return t.data_ptr()
+
+
+def _rows(t, d: int, dev, dtype, what: str):
+    """(rows, row stride) of a [..., d] tensor: contiguous, or two-dimensional
+    with contiguous rows."""
+    _arg(t.dtype == dtype and t.device == dev, f"{what}: dtype {dtype} on {dev}")
+    _arg(t.dim() >= 1 and t.shape[-1] == d, f"{what}: last dim {d}")
+    if t.is_contiguous():
+        return t.numel() // d, d
+    _arg(t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= d,
+         f"{what}: contiguous, or two-dimensional with contiguous rows")
+    return t.shape[0], t.stride(0)
+
+
+def _fp8_out(rows_shape, d: int, dev, codes, scales, block_rows=1):
+    """Code and scale outputs ([rows..., d], [row blocks..., ceil(d / 128)])."""
+    nb = (d + 127) // 128
+    cs = tuple(rows_shape) + (d,)
+    ss = (tuple(rows_shape) if block_rows == 1
+          else ((rows_shape[0] + 127) // 128,)) + (nb,)
+    if codes is None:
+        codes = torch.empty(cs, dtype=torch.float8_e4m3fn, device=dev)
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.float8_e8m0fnu, device=dev)
+    return codes, scales, _fp8(codes, cs, dev, "codes"), _fp8(scales, ss, dev, "scales")
+
+
+def _cuda(t, what: str):
+    _arg(t.is_cuda, f"{what}: tensors must live on a CUDA device")
+    return t.device
+
+
+def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, codes=None,
+                scales=None, stream=None):
+    """RMSNorm of x [..., d] (+ residual) times gain [d] fp32, as FP8
+    activations: codes [..., d] float8_e4m3fn and scales [..., ceil(d/128)]
+    float8_e8m0fnu.  With a residual also returns x + residual (in ``sum_out``,
+    which may be x or residual itself)."""
+    dev = _cuda(x, "rmsnorm_fp8")
+    dt = _dt(x)
+    _arg(x.dim() >= 1 and x.shape[-1] > 0, "x: [..., d]")
+    d = x.shape[-1]
+    T, x_ld = _rows(x, d, dev, x.dtype, "x")
+    r_ld = s_ld = 0
+    if residual is not None:
+        _arg(residual.shape == x.shape, "residual: x's shape")
+        r_ld = _rows(residual, d, dev, x.dtype, "residual")[1]
+        if sum_out is None:
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        _arg(sum_out.shape == x.shape, "sum_out: x's shape")
+        s_ld = _rows(sum_out, d, dev, x.dtype, "sum_out")[1]
+    else:
+        _arg(sum_out is None, "sum_out needs a residual")
+    if gain is not None:
+        _arg(gain.dtype == torch.float32 and tuple(gain.shape) == (d,) and gain.is_contiguous()
+             and gain.device == dev, "gain: [d] float32")
+    codes, scales, pc, ps = _fp8_out(x.shape[:-1], d, dev, codes, scales)
+    _launch(dev, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, dt, T, d, x.data_ptr(), x_ld,
+            None if residual is None else residual.data_ptr(), r_ld,
+            None if gain is None else gain.data_ptr(), eps,
+            None if sum_out is None else sum_out.data_ptr(), s_ld, pc, ps)
+    return (codes, scales) if sum_out is None else (codes, scales, sum_out)
+
+
+def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
+    """FP8 activations of x [..., d] (block_rows 1), or FP8 weights of x
+    [rows, d] (block_rows 128): codes and scales [ceil(rows/128), ceil(d/128)]."""
+    dev = _cuda(x, "fp8_quantize")
+    dt = _dt(x)
+    _arg(x.dim() >= 1 and x.shape[-1] > 0, "x: [..., d]")
+    _arg(block_rows == 1 or x.dim() == 2, "weights: [rows, d]")
+    d = x.shape[-1]
+    rows, ld = _rows(x, d, dev, x.dtype, "x")
+    codes, scales, pc, ps = _fp8_out(x.shape[:-1], d, dev, codes, scales, block_rows)
+    _launch(dev, stream, "fp8_quantize", lib().fp8_quantize, dt, rows, d, x.data_ptr(), ld,
+            block_rows, pc, ps)
+    return codes, scales
+
+
+def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y=None, ws=None,
+               stream=None):
+    """y = x w^T of FP8 activations (codes [..., K], scales [..., ceil(K/128)])
+    and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
+    bf16 or fp32.  ``y`` may be a two-dimensional column slice of a wider buffer."""
+    dev = _cuda(x_codes, "fp8_matmul")
+    _arg(x_codes.dim() >= 1 and w_codes.dim() == 2, "x_codes: [..., K], w_codes: [N, K]")
+    lead, K = tuple(x_codes.shape[:-1]), x_codes.shape[-1]
+    N, nb = w_codes.shape[0], (K + 127) // 128
+    px = _fp8(x_codes, lead + (K,), dev, "x_codes")
+    pxs = _fp8(x_scales, lead + (nb,), dev, "x_scales")
+    pw = _fp8(w_codes, (N, K), dev, "w_codes")
+    pws = _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales")
+    if y is None:
+        y = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
+    _arg(tuple(y.shape) == lead + (N,), f"y: shape {lead + (N,)}")
+    M = 1
+    for n in lead:
+        M *= n
+    y_ld = _rows(y, N, dev, y.dtype, "y")[1] if N else 0
+    if ws is None:
+        ws = workspace(256, dev)
+    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), M, N, K, px, pxs, pw, pws,
+            y.data_ptr(), y_ld, _ws(ws, dev), ws.numel())
+    return y
+
+
+def _ws(ws, dev):
+    _arg(ws.dtype == torch.uint8 and ws.device == dev and ws.is_contiguous(), f"ws: uint8 on {dev}")
+    return ws.data_ptr()
+
+
+def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scales, y=None,
+                                  ws=None, stream=None):
+    """Grouped output projection in FP8: o [T, H, c] (bf16 or fp32), w_group
+    [g, d_g, (H/g) c] and w_out [d, g d_g] FP8 weights (the scales of w_group
+    [g, d_g/128, (H/g) c/128]) -> y [T, d] bf16."""
+    dev = _cuda(o, "grouped_output_projection_fp8")
+    _arg(o.dim() == 3 and w_group.dim() == 3 and w_out.dim() == 2,
+         "o: [T, H, c], w_group: [g, d_g, k], w_out: [d, g d_g]")
+    T, H, c = o.shape
+    g, dg, kg = w_group.shape
+    d = w_out.shape[0]
+    _arg(o.is_contiguous() and g * kg == H * c, "o: contiguous, H c = g k")
+    if kg % 128 or dg % 128:
+        raise CSAError(CSA_E_UNSUPPORTED, "grouped_output_projection_fp8: (H/g) c and d_g are "
+                       "multiples of 128")
+    pg = _fp8(w_group, (g, dg, kg), dev, "w_group")
+    pgs = _fp8(w_group_scales, (g, dg // 128, kg // 128), dev, "w_group_scales")
+    po = _fp8(w_out, (d, g * dg), dev, "w_out")
+    pos = _fp8(w_out_scales, ((d + 127) // 128, g * dg // 128), dev, "w_out_scales")
+    if y is None:
+        y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
+    _arg(tuple(y.shape) == (T, d) and y.dtype == torch.bfloat16 and y.is_contiguous()
+         and y.device == dev, "y: [T, d] bf16")
+    if ws is None:
+        ws = workspace(csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, _dt(o), 1, T, H, c, g * dg), dev)
+    _launch(dev, stream, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
+            _dt(o), T, H, c, g, dg, d, o.data_ptr(), pg, pgs, po, pos, y.data_ptr(),
+            _ws(ws, dev), ws.numel())
+    return y

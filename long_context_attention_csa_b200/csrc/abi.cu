@@ -4,6 +4,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "fp8.h"
 #include "sm100.cuh"
 #include "internal.h"
 #include "tc.h"
@@ -357,6 +358,154 @@ csa_status grouped_output_projection(int32_t dtype, int64_t T, int32_t H, int32_
   return cuda_status(e);
 }
 
+// Row strides in elements of dtype: rows start on 16-byte boundaries.
+static bool row_stride_ok(int32_t dtype, int64_t ld, int64_t d) {
+  return ld >= d && ld % (dtype == CSA_BF16 ? 8 : 4) == 0;
+}
+
+csa_status rmsnorm_fp8(int32_t dtype, int64_t T, int32_t d, const void* x, int64_t x_ld,
+                       const void* residual, int64_t res_ld, const float* gain, float eps,
+                       void* sum_out, int64_t sum_ld, void* codes, void* scales, void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_E_ARG;
+  if (T < 0 || d < 1 || !(eps >= 0.f)) return CSA_E_ARG;
+  if (!row_stride_ok(dtype, x_ld, d) || (residual && !row_stride_ok(dtype, res_ld, d)) ||
+      (sum_out && (!residual || !row_stride_ok(dtype, sum_ld, d))))
+    return CSA_E_ARG;
+  if (d % 16 != 0 || d > kFp8MaxNormDim || T > 0x7fffffffLL) return CSA_E_UNSUPPORTED;
+  if (T == 0) return CSA_OK;
+  if (!x || !codes || !scales) return CSA_E_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(sum_out) ||
+      !aligned16(codes))
+    return CSA_E_ARG;
+  NormParams p{};
+  p.T = T;
+  p.d = d;
+  p.x = x;
+  p.x_ld = x_ld;
+  p.residual = residual;
+  p.res_ld = res_ld;
+  p.gain = gain;
+  p.eps = eps;
+  p.sum_out = sum_out;
+  p.sum_ld = sum_ld;
+  p.codes = codes;
+  p.scales = scales;
+  g_launches.fetch_add(1);
+  return cuda_status(launch_rmsnorm_fp8(dtype, p, S(stream)));
+}
+
+csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, int64_t ld,
+                        int32_t block_rows, void* codes, void* scales, void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_E_ARG;
+  if (rows < 0 || d < 1 || (block_rows != 1 && block_rows != 128)) return CSA_E_ARG;
+  if (!row_stride_ok(dtype, ld, d)) return CSA_E_ARG;
+  if (d % 16 != 0 || rows > 0x7fffffffLL) return CSA_E_UNSUPPORTED;
+  if (rows == 0) return CSA_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return CSA_E_ARG;
+  g_launches.fetch_add(1);
+  return cuda_status(launch_fp8_quantize(dtype, x, ld, rows, d, block_rows, codes, scales,
+                                         S(stream)));
+}
+
+csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const void* x_codes,
+                      const void* x_scales, const void* w_codes, const void* w_scales, void* y,
+                      int64_t y_ld, void* ws, size_t ws_bytes, void* stream) {
+  if (out_dtype != CSA_F32 && out_dtype != CSA_BF16) return CSA_E_ARG;
+  if (M < 0 || N < 0 || K < 1 || y_ld < N) return CSA_E_ARG;
+  if (K % 16 != 0 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
+    return CSA_E_UNSUPPORTED;
+  if (M == 0 || N == 0) return CSA_OK;
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return CSA_E_ARG;
+  if (!aligned16(x_codes) || !aligned16(w_codes) ||
+      (reinterpret_cast<uintptr_t>(y) & (out_dtype == CSA_BF16 ? 1u : 3u)) != 0)
+    return CSA_E_ARG;
+  if (!ws || ws_bytes < kWsScratch) return CSA_E_WORKSPACE;
+  Fp8GemmParams p{};
+  p.M = M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.Z = 1;
+  p.x = static_cast<const uint8_t*>(x_codes);
+  p.x_sf = static_cast<const uint8_t*>(x_scales);
+  p.x_cols = (int)K;
+  p.w = static_cast<const uint8_t*>(w_codes);
+  p.w_sf = static_cast<const uint8_t*>(w_scales);
+  p.out_dtype = out_dtype;
+  p.y = y;
+  p.y_ld = y_ld;
+  p.status = status_word(ws);
+  g_launches.fetch_add(1);
+  return cuda_status(launch_fp8_gemm(p, S(stream)));
+}
+
+// Workspace of grouped_output_projection_fp8: past the status word the codes
+// and scales of o and v, each on a 256-byte boundary.
+static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, int32_t c,
+                                         int32_t g, int32_t d_g, int32_t d, const void* o,
+                                         const void* w_group, const void* w_group_scales,
+                                         const void* w_out, const void* w_out_scales, void* y,
+                                         void* ws, size_t ws_bytes, void* stream) {
+  if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_E_ARG;
+  if (T < 0 || H <= 0 || c <= 0 || g <= 0 || d_g <= 0 || d <= 0) return CSA_E_ARG;
+  const int64_t hc = (int64_t)H * c, gd = (int64_t)g * d_g;
+  if (H % g != 0 || (hc / g) % 128 != 0 || d_g % 128 != 0) return CSA_E_UNSUPPORTED;
+  if (T > 0x7fffffffLL || hc > 0x7fffffffLL || gd > 0x7fffffffLL || g > 65535)
+    return CSA_E_UNSUPPORTED;
+  if (T == 0) return CSA_OK;
+  if (!o || !w_group || !w_group_scales || !w_out || !w_out_scales || !y) return CSA_E_ARG;
+  if (!aligned16(o) || !aligned16(w_group) || !aligned16(w_out) || !aligned16(y))
+    return CSA_E_ARG;
+  if (!ws || !aligned16(ws) ||
+      ws_bytes < csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dtype, 1, T, H, c, gd, 0, 0))
+    return CSA_E_WORKSPACE;
+  uint8_t* oc = static_cast<uint8_t*>(ws) + kWsScratch;
+  uint8_t* os = oc + up256((size_t)T * hc);
+  uint8_t* vc = os + up256((size_t)T * (hc / 128));
+  uint8_t* vs = vc + up256((size_t)T * gd);
+  float* v = reinterpret_cast<float*>(vs + up256((size_t)T * (gd / 128)));
+  cudaError_t e = launch_fp8_quantize(dtype, o, hc, T, (int)hc, 1, oc, os, S(stream));
+  if (e != cudaSuccess) return CSA_E_CUDA;
+  g_launches.fetch_add(1);
+  Fp8GemmParams p{};
+  p.M = T;
+  p.N = d_g;
+  p.K = (int)(hc / g);
+  p.Z = g;
+  p.x = oc;
+  p.x_sf = os;
+  p.x_cols = (int)hc;
+  p.x_koff = p.K;
+  p.w = static_cast<const uint8_t*>(w_group);
+  p.w_sf = static_cast<const uint8_t*>(w_group_scales);
+  p.out_dtype = CSA_F32;
+  p.y = v;
+  p.y_ld = gd;
+  p.y_noff = d_g;
+  p.status = status_word(ws);
+  e = launch_fp8_gemm(p, S(stream));
+  if (e != cudaSuccess) return CSA_E_CUDA;
+  g_launches.fetch_add(1);
+  e = launch_fp8_quantize(CSA_F32, v, gd, T, (int)gd, 1, vc, vs, S(stream));
+  if (e != cudaSuccess) return CSA_E_CUDA;
+  g_launches.fetch_add(1);
+  p.N = d;
+  p.K = p.x_cols = (int)gd;
+  p.Z = 1;
+  p.x = vc;
+  p.x_sf = vs;
+  p.x_koff = p.y_noff = 0;
+  p.w = static_cast<const uint8_t*>(w_out);
+  p.w_sf = static_cast<const uint8_t*>(w_out_scales);
+  p.out_dtype = CSA_BF16;
+  p.y = y;
+  p.y_ld = d;
+  e = launch_fp8_gemm(p, S(stream));
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  return cuda_status(e);
+}
+
 size_t csa_workspace_bytes(int32_t op, int32_t dtype, int64_t B, int64_t Tq, int32_t H, int32_t c,
                            int64_t N, int32_t k, int32_t n_win) {
   if (B < 0 || Tq < 0 || N < 0) return 0;
@@ -367,6 +516,14 @@ size_t csa_workspace_bytes(int32_t op, int32_t dtype, int64_t B, int64_t Tq, int
       return kWsScratch + indexer_mx_scratch(B, Tq, N, k);
     case CSA_OP_OUT_PROJ:
       return kWsScratch + (size_t)B * (size_t)Tq * (size_t)N * 2;
+    case CSA_OP_FP8_MATMUL:
+      return kWsScratch;
+    case CSA_OP_OUT_PROJ_FP8: {
+      if (H < 0 || c < 0) return 0;
+      const size_t T = (size_t)B * (size_t)Tq, hc = (size_t)H * (size_t)c;
+      return kWsScratch + up256(T * hc) + up256(T * (hc / 128)) + up256(T * (size_t)N) +
+             up256(T * ((size_t)N / 128)) + T * (size_t)N * 4;
+    }
     case CSA_OP_INDEXER:
       return kWsScratch + (dtype == CSA_BF16 ? indexer_tc_scratch(B, Tq, N, k)
                                              : indexer_portable_scratch(B, Tq, N, k));

@@ -1,0 +1,49 @@
+// The 8-bit projection path: E4M3 codes with a power-of-two scale per 128
+// columns (activations: of one row; weights: of 128 rows).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace csa {
+
+constexpr int kFp8MaxNormDim = 32768;   // columns rmsnorm_fp8 holds in registers
+
+struct NormParams {
+  int64_t T;
+  int d;
+  const void* x;          // [T, d], row stride x_ld elements
+  int64_t x_ld;
+  const void* residual;   // or null
+  int64_t res_ld;
+  const float* gain;      // [d] or null
+  float eps;
+  void* sum_out;          // [T, d] or null
+  int64_t sum_ld;
+  void* codes;            // [T, d]
+  void* scales;           // [T, ceil(d / 128)]
+};
+cudaError_t launch_rmsnorm_fp8(int dtype, const NormParams& p, cudaStream_t stream);
+
+cudaError_t launch_fp8_quantize(int dtype, const void* x, int64_t ld, int64_t rows, int d,
+                                int block_rows, void* codes, void* scales, cudaStream_t stream);
+
+// Y[m, z y_noff + n] = sum_k X[m, z x_koff + k] W[z][n, k], n < N, k < K.
+struct Fp8GemmParams {
+  int64_t M;
+  int N, K, Z;
+  const uint8_t* x;        // [M, x_cols] codes
+  const uint8_t* x_sf;     // [M, ceil(x_cols / 128)]
+  int x_cols;
+  int x_koff;              // per z, a multiple of 128
+  const uint8_t* w;        // [Z, N, K] codes
+  const uint8_t* w_sf;     // [Z, ceil(N / 128), ceil(K / 128)]
+  int out_dtype;           // CSA_F32 or CSA_BF16
+  void* y;
+  int64_t y_ld;
+  int y_noff;              // per z
+  unsigned* status;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream);
+
+}  // namespace csa

@@ -440,3 +440,71 @@ def grouped_output_projection(o, w_group, w_out) -> np.ndarray:
     u = o.reshape(T, g, (H // g) * c)                     # each group's heads, concatenated
     v = np.einsum("tgi,gdi->tgd", u, w_group)            # [T, g, d_g]
     return v.reshape(T, g * dg) @ w_out.T
+
+
+# ---- the 8-bit projection path -----------------------------------------------
+
+def _fp8_blocks(x, block_rows: int):
+    """x [R, d] filled up with zeros, as [R / block_rows, block_rows, d / 128, 128]."""
+    R, d = x.shape
+    nr, nc = -(-R // block_rows), -(-d // 128)
+    full = np.zeros((nr * block_rows, nc * 128))
+    full[:R, :d] = x
+    return full.reshape(nr, block_rows, nc, 128)
+
+
+def fp8_exponents(x, block_rows: int = 1) -> np.ndarray:
+    """Scale exponents of x [R, d]: for each block of block_rows rows and 128
+    columns the smallest e >= -127 with amax <= 448 2^e, amax over the block's
+    finite elements; -127 where that is zero."""
+    b = np.abs(_fp8_blocks(_f64(x), block_rows))
+    amax = np.where(np.isfinite(b), b, 0.0).max(axis=(1, 3))
+    f, ex = np.frexp(amax)                    # amax = f 2^ex, 1/2 <= f < 1; 448 = 7/8 2^9
+    e = ex - 9 + (f > 0.875)
+    return np.where(amax > 0, np.maximum(e, -127), -127).astype(np.int64)
+
+
+def _fp8_spread(e, block_rows: int, shape) -> np.ndarray:
+    e = np.repeat(np.repeat(e, block_rows, axis=0), 128, axis=1)
+    return e[:shape[0], :shape[1]]
+
+
+def e4m3_round(r) -> np.ndarray:
+    """Nearest E4M3 values of |r| <= 448, ties to even; NaN where r is not finite."""
+    r = _f64(r)
+    a = np.where(np.isfinite(r), np.abs(r), 1.0)
+    step = np.ldexp(1.0, np.maximum(np.frexp(a)[1] - 1, -6) - 3)
+    q = np.copysign(np.rint(a / step) * step, r)
+    return np.where(np.isfinite(r), q, np.nan)
+
+
+def fp8_quantize(x, block_rows: int = 1):
+    """(values [R, d] of the E4M3 codes, scale exponents) of x [R, d]."""
+    x = _f64(x)
+    e = fp8_exponents(x, block_rows)
+    return e4m3_round(np.ldexp(x, -_fp8_spread(e, block_rows, x.shape))), e
+
+
+def fp8_values(codes, e, block_rows: int = 1) -> np.ndarray:
+    """The numbers that E4M3 values `codes` [R, d] with exponents e stand for."""
+    codes = _f64(codes)
+    return np.ldexp(codes, _fp8_spread(np.asarray(e, dtype=np.int64), block_rows, codes.shape))
+
+
+def rmsnorm_residual(x, residual=None, gain=None, eps: float = 1e-6):
+    """(h, y): h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain, rows of [T, d]."""
+    h = _f64(x) if residual is None else _f64(x) + _f64(residual)
+    y = h / np.sqrt((h * h).mean(axis=-1, keepdims=True) + eps)
+    return h, (y if gain is None else y * _f64(gain))
+
+
+def grouped_output_projection_fp8(o, w_group, w_out) -> np.ndarray:
+    """grouped_output_projection with each row of o and of the concatenated
+    intermediate v held in FP8 (blocks of 128 columns); w_group and w_out are
+    the values their codes stand for."""
+    o, w_group, w_out = _f64(o), _f64(w_group), _f64(w_out)
+    T = o.shape[0]
+    g, dg, gin = w_group.shape
+    u = fp8_values(*fp8_quantize(o.reshape(T, -1))).reshape(T, g, gin)
+    v = np.einsum("tgi,gdi->tgd", u, w_group).reshape(T, g * dg)
+    return fp8_values(*fp8_quantize(v)) @ w_out.T
