@@ -430,7 +430,7 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
   p.x_cols = (int)K;
   p.w = static_cast<const uint8_t*>(w_codes);
   p.w_sf = static_cast<const uint8_t*>(w_scales);
-  p.out_dtype = out_dtype;
+  p.out = out_dtype;
   p.y = y;
   p.y_ld = y_ld;
   p.status = status_word(ws);
@@ -464,7 +464,6 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   uint8_t* os = oc + up256((size_t)T * hc);
   uint8_t* vc = os + up256((size_t)T * (hc / 128));
   uint8_t* vs = vc + up256((size_t)T * gd);
-  float* v = reinterpret_cast<float*>(vs + up256((size_t)T * (gd / 128)));
   cudaError_t e = launch_fp8_quantize(dtype, o, hc, T, (int)hc, 1, oc, os, S(stream));
   if (e != cudaSuccess) return CSA_E_CUDA;
   g_launches.fetch_add(1);
@@ -479,15 +478,13 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   p.x_koff = p.K;
   p.w = static_cast<const uint8_t*>(w_group);
   p.w_sf = static_cast<const uint8_t*>(w_group_scales);
-  p.out_dtype = CSA_F32;
-  p.y = v;
+  p.out = kFp8Out;
+  p.y = vc;
+  p.y_sf = vs;
   p.y_ld = gd;
   p.y_noff = d_g;
   p.status = status_word(ws);
   e = launch_fp8_gemm(p, S(stream));
-  if (e != cudaSuccess) return CSA_E_CUDA;
-  g_launches.fetch_add(1);
-  e = launch_fp8_quantize(CSA_F32, v, gd, T, (int)gd, 1, vc, vs, S(stream));
   if (e != cudaSuccess) return CSA_E_CUDA;
   g_launches.fetch_add(1);
   p.N = d;
@@ -498,7 +495,7 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   p.x_koff = p.y_noff = 0;
   p.w = static_cast<const uint8_t*>(w_out);
   p.w_sf = static_cast<const uint8_t*>(w_out_scales);
-  p.out_dtype = CSA_BF16;
+  p.out = CSA_BF16;
   p.y = y;
   p.y_ld = d;
   e = launch_fp8_gemm(p, S(stream));
@@ -522,7 +519,7 @@ size_t csa_workspace_bytes(int32_t op, int32_t dtype, int64_t B, int64_t Tq, int
       if (H < 0 || c < 0) return 0;
       const size_t T = (size_t)B * (size_t)Tq, hc = (size_t)H * (size_t)c;
       return kWsScratch + up256(T * hc) + up256(T * (hc / 128)) + up256(T * (size_t)N) +
-             up256(T * ((size_t)N / 128)) + T * (size_t)N * 4;
+             up256(T * ((size_t)N / 128));
     }
     case CSA_OP_INDEXER:
       return kWsScratch + (dtype == CSA_BF16 ? indexer_tc_scratch(B, Tq, N, k)

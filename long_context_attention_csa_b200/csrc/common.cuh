@@ -164,6 +164,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
 // Sum of `v` over each group of LPR consecutive threads (LPR a power of two,
 // blockDim.x a multiple of LPR).  Every thread of the block must call it
 // (it contains __syncthreads when LPR > 32).  `red` holds blockDim.x/32 floats.

@@ -7,10 +7,9 @@
 // x 2^-e rounded to nearest even, so no finite element saturates and a normal
 // code's relative error is at most 2^-4 whatever the scale.  NaN and infinity
 // become the NaN code and do not touch the scale.
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 #include "fp8.h"
+#include "fp8_codes.cuh"
 #include "internal.h"
 
 namespace csa {
@@ -50,25 +49,6 @@ __device__ __forceinline__ void drop_inf8(float* v) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i)
     if (isinf(v[i])) v[i] = __int_as_float(0x7fffffff);
-}
-
-// e + 127 of a finite amax = 1.m 2^x: 448 = 1.75 2^8, so e = x - 8, one more
-// when 1.m > 1.75; amax below 448 2^-127 (zero and subnormals included) gives 0.
-__device__ __forceinline__ uint32_t scale_byte(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return e > 0 ? (uint32_t)e : 0u;
-}
-
-// Codes of v 2^-e (an exact product: the factor is a normal power of two).
-__device__ __forceinline__ uint2 codes8(const float* v, uint32_t byte) {
-  const float f = __uint_as_float((254u - byte) << 23);   // 2^(127 - byte), byte <= 247
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * f, v[2 * i + 1] * f),
-                                              __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
 // Block scale and codes of this lane's eight elements.  Every lane of the warp

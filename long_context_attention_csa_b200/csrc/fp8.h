@@ -28,6 +28,8 @@ cudaError_t launch_rmsnorm_fp8(int dtype, const NormParams& p, cudaStream_t stre
 cudaError_t launch_fp8_quantize(int dtype, const void* x, int64_t ld, int64_t rows, int d,
                                 int block_rows, void* codes, void* scales, cudaStream_t stream);
 
+constexpr int kFp8Out = 2;   // Y as E4M3 codes with their own scales
+
 // Y[m, z y_noff + n] = sum_k X[m, z x_koff + k] W[z][n, k], n < N, k < K.
 struct Fp8GemmParams {
   int64_t M;
@@ -38,8 +40,9 @@ struct Fp8GemmParams {
   int x_koff;              // per z, a multiple of 128
   const uint8_t* w;        // [Z, N, K] codes
   const uint8_t* w_sf;     // [Z, ceil(N / 128), ceil(K / 128)]
-  int out_dtype;           // CSA_F32 or CSA_BF16
-  void* y;
+  int out;                 // CSA_F32, CSA_BF16, or kFp8Out
+  void* y;                 // kFp8Out: codes (N, y_ld and y_noff multiples of 128)
+  uint8_t* y_sf;           // kFp8Out: their scales [M, y_ld / 128]
   int64_t y_ld;
   int y_noff;              // per z
   unsigned* status;

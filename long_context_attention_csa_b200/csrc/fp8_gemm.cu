@@ -1,95 +1,712 @@
 // Matrix product of E4M3 operands with a power-of-two scale per 128 columns
-// (one row of X; 128 rows of W): y[m, n] = sum_b 2^(ex[m,b] + ew[n/128,b])
-// sum_{k in b} x[m,k] w[n,k].  The block's products are summed in float32
-// (they are exact there up to 2^24 steps of the smallest product), the scale
-// applied once per block and the blocks summed in float32.
+// (of one row of X, of 128 rows of W) on the block-scaled 5th-generation
+// tensor cores:
+//   Y[m, n] = sum_b 2^(ex[m,b] + ew[n/128,b]) sum_{k in block b} X[m,k] W[n,k],
+// products and sums in float32 (kind::mxf8f6f4.block_scale; accumulators in
+// TMEM), rounded once on the way out: bf16, float32, or E4M3 again with its own
+// scales (the grouped projection's intermediate).
+//
+// Scales.  The MMA takes one scale byte per row and 32 columns; a block of 128
+// columns is four MMAs (K = 32 each) that use the same byte.  So one TMEM word
+// per row holds the bytes of four consecutive blocks (512 columns, a "chunk"),
+// and the MMA descriptor's scale index picks block kb mod 4.  The scales stay
+// in their natural layout in memory; one warp turns a chunk's words into the
+// 512-byte tile of the tensor cores (row r's word at byte 16 (r mod 32) + 4
+// (r div 32)) and tcgen05.cp brings it into TMEM, two chunks deep.
+//
+// Two kernels.  fp8_gemm_kernel: many rows, X rows on the MMA's M, 256 columns
+// on N, persistent.  fp8_gemm_few_kernel: few rows, where the bytes of W are
+// the bound: W rows on M, the few X rows on N, K split over a cluster.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "fp8.h"
+#include "fp8_codes.cuh"
 #include "internal.h"
+#include "sm100.cuh"
+#include "tma_host.h"
 
 namespace csa {
 
 namespace {
 
-constexpr int kT = 64;    // tile rows and columns
-constexpr int kTK = 32;   // K per step
+using namespace sm100;
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+constexpr int kBK = 128;          // columns per stage: one 128-byte swizzled row, one scale block
+constexpr int kChunk = 4;         // scale blocks per TMEM word
+constexpr int kTileM = 128;       // MMA M
+constexpr int kTileA = kTileM * kBK;
+
+// Scale bytes 4 c .. 4 c + 3 of a row of scales: block b's byte in byte b mod 4.
+// Bytes at or past `end` (the row's blocks) are not read.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int b0, int end, bool words) {
+  if (words) return *reinterpret_cast<const uint32_t*>(row + b0);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < kChunk; ++i)
+    if (b0 + i < end) w |= (uint32_t)row[b0 + i] << (8 * i);
+  return w;
 }
 
-__device__ __forceinline__ float pow2(uint8_t byte) {
-  return byte == 255 ? __int_as_float(0x7fffffff) : exp2f((float)byte - 127.f);
+struct GemmArgs {
+  Fp8GemmParams p;
+  int kb_n;              // scale blocks (stages) of K
+  int x_blocks;          // scale blocks of a row of X
+  int w_rblocks;         // scale block rows of one W
+  bool x_words, w_words; // scale rows start on 4-byte boundaries and end on them
+  bool vec;              // rows of Y start on 16-byte boundaries
+  int64_t tiles;
+  int m_tiles, n_tiles;
+};
+
+// 2^e of the block and codes of 128 consecutive values of one row.
+__device__ __forceinline__ void store_codes128(const float* v, uint8_t* codes, uint8_t* scale) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 128; ++i) a = fmaxf(a, fabsf(v[i]));
+  if (isinf(a)) {
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) a = fmaxf(a, isinf(v[i]) ? 0.f : fabsf(v[i]));
+  }
+  const uint32_t byte = scale_byte(a);
+  *scale = (uint8_t)byte;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint2 lo = codes8(v + 16 * q, byte), hi = codes8(v + 16 * q + 8, byte);
+    reinterpret_cast<uint4*>(codes)[q] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
 }
 
-__global__ void __launch_bounds__(256) fp8_gemm_kernel(Fp8GemmParams p) {
-  __shared__ float xs[kTK][kT + 1], ws[kTK][kT + 1];
-  pdl_wait();
-  const int64_t m0 = (int64_t)blockIdx.x * kT;
-  const int n0 = blockIdx.y * kT, z = blockIdx.z;
-  const int xb = (p.x_cols + 127) / 128, wb = (p.K + 127) / 128, wrb = (p.N + 127) / 128;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {}, part[4][4] = {};
-  for (int k0 = 0; k0 < p.K; k0 += kTK) {
-    for (int i = threadIdx.x; i < kT * kTK; i += 256) {
-      const int r = i / kTK, k = i % kTK;
-      const int64_t m = m0 + r;
-      const int n = n0 + r;
-      xs[k][r] = m < p.M && k0 + k < p.K
-                     ? e4m3(p.x[m * p.x_cols + (int64_t)z * p.x_koff + k0 + k]) : 0.f;
-      ws[k][r] = n < p.N && k0 + k < p.K
-                     ? e4m3(p.w[((int64_t)z * p.N + n) * p.K + k0 + k]) : 0.f;
+// Thirty-two consecutive values of one row, `n` of them inside Y.
+template <int OUT>
+__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r, int n,
+                                            bool vec) {
+  if constexpr (OUT == CSA_BF16) {
+    bf16* dst = static_cast<bf16*>(y) + at;
+    if (vec && n >= 32) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        reinterpret_cast<uint4*>(dst)[q] = make_uint4(
+            pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
+            pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
+            pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
+            pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) dst[i] = __float2bfloat16_rn(__uint_as_float(r[i]));
     }
-    __syncthreads();
+  } else {
+    float* dst = static_cast<float*>(y) + at;
+    if (vec && n >= 32) {
 #pragma unroll
-    for (int k = 0; k < kTK; ++k)
+      for (int q = 0; q < 8; ++q)
+        reinterpret_cast<uint4*>(dst)[q] =
+            make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+    } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          part[i][j] = fmaf(xs[k][ty * 4 + i], ws[k][tx * 4 + j], part[i][j]);
-    __syncthreads();
-    if ((k0 + kTK) % 128 == 0 || k0 + kTK >= p.K) {
-      const int kb = k0 / 128;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t m = m0 + ty * 4 + i;
-          const int n = n0 + tx * 4 + j;
-          if (m < p.M && n < p.N) {
-            const float sx = pow2(p.x_sf[m * xb + z * (p.x_koff / 128) + kb]);
-            const float sw = pow2(p.w_sf[((int64_t)z * wrb + n / 128) * wb + kb]);
-            acc[i][j] += part[i][j] * sx * sw;
-          }
-          part[i][j] = 0.f;
-        }
+      for (int i = 0; i < 32; ++i)
+        if (i < n) dst[i] = __uint_as_float(r[i]);
     }
   }
+}
+
+// ---- many rows ----------------------------------------------------------------
+//
+// Persistent CTAs walk 128 x 256 tiles, n fastest (the CTAs that run at once
+// share their X tiles and all of W through L2).
+//   warp 0     TMA producer, a four-slot ring of K blocks (16 + 32 KB)
+//   warp 1     TMEM owner, single-thread MMA issuer
+//   warp 2     scale tiles
+//   warps 4-7  epilogue, thread = row
+// The two 256-column accumulators and the scales' 24 columns do not fit 512, so
+// the accumulators share 24 columns: the epilogue reads those first and only
+// then lets the next tile's MMAs begin.
+constexpr int kN = 256;
+constexpr int kStages = 4;
+constexpr int kStage = kTileA + kN * kBK;
+constexpr int kSfSlot = 512 + kN / 128 * 512;
+constexpr int kOffSf = kStages * kStage;
+constexpr int kOffBar = kOffSf + 2 * kSfSlot;
+constexpr int kSmem = kOffBar + 256;
+constexpr int kThreads = 256;
+constexpr uint32_t kAcc1 = 232;               // second accumulator: columns 232 .. 487
+constexpr uint32_t kSfCol = 488;              // scales: 2 x (4 + 8) columns
+static_assert(kSmem + 1024 <= 232448, "shared memory budget");
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_x,
+                    const __grid_constant__ CUtensorMap map_w, GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kOffBar);   // [stages] operands landed
+  uint64_t* empty = full + kStages;         // [stages] operands consumed
+  uint64_t* sfull = empty + kStages;        // [2] scale tiles written
+  uint64_t* sempty = sfull + 2;             // [2] the chunk's MMAs are done
+  uint64_t* tfull = sempty + 2;             // accumulator complete
+  uint64_t* tfree = tfull + 1;              // the shared columns have been read
+  uint64_t* drain = tfree + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Fp8GemmParams& p = a.p;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tfree, 128);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  auto tile_of = [&](int64_t u, int& z, int64_t& m0, int& n0) {
+    const int nt = (int)(u % a.n_tiles);
+    const int64_t r = u / a.n_tiles;
+    m0 = (r % a.m_tiles) * kTileM;
+    z = (int)(r / a.m_tiles);
+    n0 = nt * kN;
+  };
+  auto give_up = [&](unsigned where) {
+    *abort_flag = 1;
+    report(p.status, CSA_DEV_TIMEOUT, where);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      for (int64_t u = blockIdx.x; u < a.tiles && !*abort_flag; u += gridDim.x) {
+        int z, n0;
+        int64_t m0;
+        tile_of(u, z, m0, n0);
+        for (int kb = 0; kb < a.kb_n; ++kb) {
+          const uint32_t s = it % kStages;
+          if (*abort_flag || !mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u)) {
+            give_up(0x801u);
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], kStage);
+          uint8_t* dst = sm + s * kStage;
+          tma_load_3d(dst, &map_x, &full[s], z * p.x_koff + kb * kBK, (int32_t)m0, 0);
+          tma_load_3d(dst + kTileA, &map_w, &full[s], kb * kBK, n0, z);
+          ++it;
+        }
+      }
+      // every issued copy has landed before the CTA may exit
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+        mbar_wait(&full[i % kStages], (i / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      uint32_t it = 0, ch = 0, n = 0;
+      for (int64_t u = blockIdx.x; u < a.tiles; u += gridDim.x, ++n) {
+        if (*abort_flag || (n > 0 && !mbar_wait(tfree, (n - 1) & 1u))) {
+          give_up(0x802u);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + ((n & 1u) ? kAcc1 : 0u);
+        bool ok = true;
+        for (int kb = 0; kb < a.kb_n && ok; ++kb, ++it) {
+          const uint32_t s = it % kStages, slot = ch & 1u;
+          const uint32_t sfa = tmem + kSfCol + slot * 12u, sfb = sfa + 4u;
+          if ((kb & 3) == 0) {
+            ok = !*abort_flag && mbar_wait(&sfull[slot], (ch >> 1) & 1u);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t ss = smem_u32(sm + kOffSf + slot * kSfSlot);
+              tmem_cp_32x128b_x4(sfa, smem_desc(ss, 16, 128, 0));
+              tmem_cp_32x128b_x4(sfb, smem_desc(ss + 512, 16, 128, 0));
+              tmem_cp_32x128b_x4(sfb + 4, smem_desc(ss + 1024, 16, 128, 0));
+            }
+          }
+          ok = ok && !*abort_flag && mbar_wait(&full[s], (it / kStages) & 1u);
+          if (!ok) {
+            give_up(0x803u);
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm + s * kStage);
+          const uint32_t id = (uint32_t)kb & 3u;
+          const uint32_t idesc = idesc_mxf8_e4m3(kTileM, kN, id, id);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            mma_mxf8_ss(d, smem_desc(sa + kk * 32, 16, 1024, 2),
+                        smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc, sfa | (id << 30),
+                        sfb | (id << 30), (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&empty[s]);
+          if ((kb & 3) == 3 || kb == a.kb_n - 1) {
+            mma_commit(&sempty[slot]);
+            ++ch;
+          }
+        }
+        if (!ok) break;
+        mma_commit(tfull);
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+  } else if (warp == 2) {
+    // scale tiles: a lane holds rows lane, lane + 32, ... of X; W's rows all
+    // carry their 128-row block's word
+    uint32_t ch = 0;
+    bool ok = true;
+    for (int64_t u = blockIdx.x; u < a.tiles && ok; u += gridDim.x) {
+      int z, n0;
+      int64_t m0;
+      tile_of(u, z, m0, n0);
+      const int xb0 = z * (p.x_koff / 128);
+      const uint8_t* wrow = p.w_sf + ((int64_t)z * a.w_rblocks + n0 / 128) * a.kb_n;
+      const bool second = n0 / 128 + 1 < a.w_rblocks;
+      auto load = [&](int kb, uint32_t* x, uint32_t* w) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i;
-      const int n = n0 + tx * 4 + j;
-      if (m < p.M && n < p.N) {
-        const int64_t at = m * p.y_ld + (int64_t)z * p.y_noff + n;
-        if (p.out_dtype == CSA_BF16)
-          static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(acc[i][j]);
-        else
-          static_cast<float*>(p.y)[at] = acc[i][j];
+        for (int i = 0; i < 4; ++i) {
+          const int64_t m = m0 + 32 * i + lane;
+          x[i] = m < p.M ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_words)
+                         : 0u;
+        }
+        w[0] = scale_word(wrow, kb, a.kb_n, a.w_words);
+        w[1] = second ? scale_word(wrow + a.kb_n, kb, a.kb_n, a.w_words) : 0u;
+      };
+      uint32_t x[4], w[2];
+      load(0, x, w);
+      for (int kb = 0; kb < a.kb_n; kb += kChunk, ++ch) {
+        const uint32_t slot = ch & 1u;
+        ok = __all_sync(0xffffffffu,
+                        !*abort_flag && mbar_wait(&sempty[slot], ((ch >> 1) & 1u) ^ 1u));
+        if (!ok) {
+          give_up(0x804u);
+          break;
+        }
+        uint4* dst = reinterpret_cast<uint4*>(sm + kOffSf + slot * kSfSlot) + lane;
+        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        dst[32] = make_uint4(w[0], w[0], w[0], w[0]);
+        dst[64] = make_uint4(w[1], w[1], w[1], w[1]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[slot]);
+        if (kb + kChunk < a.kb_n) load(kb + kChunk, x, w);
       }
     }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    uint32_t n = 0;
+    for (int64_t u = blockIdx.x; u < a.tiles; u += gridDim.x, ++n) {
+      int z, n0;
+      int64_t m0;
+      tile_of(u, z, m0, n0);
+      // warp-uniform decision: the TMEM loads below are warp-collective
+      if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(tfull, n & 1u))) {
+        give_up(0x805u);
+        break;
+      }
+      tc_fence_after();
+      const int64_t row = m0 + quarter * 32 + lane;
+      const int64_t at = row * p.y_ld + (int64_t)z * p.y_noff + n0;
+      const bool odd = (n & 1u) != 0;
+      const uint32_t base = tmem_addr(tmem, (uint32_t)(quarter * 32), odd ? kAcc1 : 0u);
+      const bool live = row < p.M;
+      if constexpr (OUT == kFp8Out) {
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int h = odd ? i : 1 - i;   // the half with the shared columns first
+          uint32_t r[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(base + h * 128 + q * 32, r + q * 32);
+          tmem_ld_wait();
+          if (i == 0) {
+            tc_fence_before();
+            mbar_arrive(tfree);
+          }
+          if (live && n0 + h * 128 < p.N)   // N is a multiple of 128
+            store_codes128(reinterpret_cast<const float*>(r),
+                           static_cast<uint8_t*>(p.y) + at + h * 128,
+                           p.y_sf + (at + h * 128) / 128);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kN / 32; ++i) {
+          const int cc = odd ? 32 * i : kN - 32 - 32 * i;   // the shared columns first
+          uint32_t r[32];
+          tmem_ld32(base + cc, r);
+          tmem_ld_wait();
+          if (i == 0) {
+            tc_fence_before();
+            mbar_arrive(tfree);
+          }
+          if (live && n0 + cc < p.N) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.vec);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---- few rows -------------------------------------------------------------------
+//
+// One CTA: 128 rows of W against up to NT rows of X over its share of K; the
+// cluster's CTAs hold the shares of one tile, leave float32 partials in shared
+// memory and add them in rank order (the sum's order does not depend on
+// timing), each for its share of the X rows.
+//   warp 0     TMA producer
+//   warp 1     TMEM owner, single-thread MMA issuer
+//   warp 2     scale tiles
+//   all four   TMEM -> shared memory -> sum over the cluster -> Y
+template <int NT>
+struct Few {
+  static constexpr int stage = kTileA + NT * kBK;
+  static constexpr int stages = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
+  static constexpr int off_sf = stages * stage;
+  static constexpr int off_bar = off_sf + 2 * 1024;
+  static constexpr int smem = off_bar + 256;
+  static constexpr uint32_t cols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
+  static constexpr uint32_t sf_col = NT;   // after the accumulator: 2 x (4 + 4) columns
+  static_assert(NT * kTileM * 4 <= stages * stage, "partials reuse the ring");
+  static_assert(2 * (smem + 1024 + 1024) <= 233472, "two CTAs per SM");
+};
+
+template <int NT, int OUT>
+__global__ void __launch_bounds__(128)
+    fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap map_x,
+                        const __grid_constant__ CUtensorMap map_w, GemmArgs a, int split) {
+  using L = Few<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::off_bar);
+  uint64_t* empty = full + L::stages;
+  uint64_t* sfull = empty + L::stages;
+  uint64_t* sempty = sfull + 2;
+  uint64_t* done = sempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Fp8GemmParams& p = a.p;
+  const int rank = (int)(blockIdx.x % split);
+  const int64_t u = blockIdx.x / split;
+  const int nt = (int)(u % a.n_tiles);
+  const int64_t m0 = (u / a.n_tiles) % a.m_tiles * NT;
+  const int z = (int)(u / a.n_tiles / a.m_tiles);
+  const int n0 = nt * kTileM;
+  // this CTA's chunks of K
+  const int chunks = (a.kb_n + kChunk - 1) / kChunk;
+  const int c0 = (int)((int64_t)chunks * rank / split);
+  const int c1 = (int)((int64_t)chunks * (rank + 1) / split);
+  const int kb0 = c0 * kChunk, kb1 = min(c1 * kChunk, a.kb_n);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sempty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&map_x);
+    tma_prefetch_desc(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, L::cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  auto give_up = [&](unsigned where) {
+    *abort_flag = 1;
+    report(p.status, CSA_DEV_TIMEOUT, where);
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t s = it % L::stages;
+        if (*abort_flag || !mbar_wait(&empty[s], ((it / L::stages) & 1u) ^ 1u)) {
+          give_up(0x811u);
+          break;
+        }
+        mbar_arrive_expect_tx(&full[s], L::stage);
+        uint8_t* dst = sm + s * L::stage;
+        tma_load_3d(dst, &map_w, &full[s], kb * kBK, n0, z);
+        tma_load_3d(dst + kTileA, &map_x, &full[s], z * p.x_koff + kb * kBK, (int32_t)m0, 0);
+        ++it;
+      }
+      for (uint32_t i = it > L::stages ? it - L::stages : 0; i < it; ++i)
+        mbar_wait(&full[i % L::stages], (i / L::stages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      uint32_t it = 0, ch = 0;
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t s = it % L::stages, slot = ch & 1u;
+        const uint32_t sfa = tmem + L::sf_col + slot * 8u, sfb = sfa + 4u;
+        bool ok = !*abort_flag;
+        if (ok && (kb & 3) == 0) {
+          ok = mbar_wait(&sfull[slot], (ch >> 1) & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint32_t ss = smem_u32(sm + L::off_sf + slot * 1024);
+            tmem_cp_32x128b_x4(sfa, smem_desc(ss, 16, 128, 0));
+            tmem_cp_32x128b_x4(sfb, smem_desc(ss + 512, 16, 128, 0));
+          }
+        }
+        if (!ok || !mbar_wait(&full[s], (it / L::stages) & 1u)) {
+          give_up(0x812u);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(sm + s * L::stage);
+        const uint32_t id = (uint32_t)kb & 3u;
+        const uint32_t idesc = idesc_mxf8_e4m3(kTileM, NT, id, id);
+#pragma unroll
+        for (int kk = 0; kk < kBK / 32; ++kk)
+          mma_mxf8_ss(tmem, smem_desc(sa + kk * 32, 16, 1024, 2),
+                      smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc, sfa | (id << 30),
+                      sfb | (id << 30), (kb > kb0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[s]);
+        if ((kb & 3) == 3) {
+          mma_commit(&sempty[slot]);
+          ++ch;
+        }
+      }
+      mma_commit(done);
+    }
+  } else if (warp == 2) {
+    const int xb0 = z * (p.x_koff / 128);
+    const uint8_t* wrow = p.w_sf + ((int64_t)z * a.w_rblocks + nt) * a.kb_n;
+    uint32_t ch = 0;
+    for (int kb = kb0; kb < kb1; kb += kChunk, ++ch) {
+      uint32_t x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t m = m0 + 32 * i + lane;
+        x[i] = 32 * i + lane < NT && m < p.M
+                   ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_words)
+                   : 0u;
+      }
+      const uint32_t w = scale_word(wrow, kb, a.kb_n, a.w_words);
+      const uint32_t slot = ch & 1u;
+      if (!__all_sync(0xffffffffu,
+                      !*abort_flag && mbar_wait(&sempty[slot], ((ch >> 1) & 1u) ^ 1u))) {
+        give_up(0x813u);
+        break;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(sm + L::off_sf + slot * 1024) + lane;
+      dst[0] = make_uint4(w, w, w, w);
+      dst[32] = make_uint4(x[0], x[1], x[2], x[3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfull[slot]);
+    }
+  }
+  __syncwarp();
+  // `done` follows every MMA, so every landed stage has been read
+  if (!__all_sync(0xffffffffu, mbar_wait(done, 0))) give_up(0x814u);
+  __syncthreads();
+  tc_fence_after();
+  float* part = reinterpret_cast<float*>(sm);   // [NT][128]
+  {
+    const uint32_t base = tmem_addr(tmem, (uint32_t)(warp * 32), 0);
+    constexpr int step = NT < 32 ? NT : 32;
+#pragma unroll 1
+    for (int t = 0; t < NT && m0 + t < p.M; t += step) {
+      uint32_t r[step];
+      if constexpr (step == 32) tmem_ld32(base + t, r);
+      else tmem_ld16(base + t, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < step; ++i)
+        part[(t + i) * kTileM + warp * 32 + lane] = __uint_as_float(r[i]);
+    }
+  }
+  tc_fence_before();
+  if (split > 1) cluster_sync();
+  else __syncthreads();
+  // a warp sums one X row's 128 columns, four a lane
+  const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+  for (int t = rank + split * warp; t < rows; t += split * 4) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < split; ++j) {
+      const uint4 q = dsmem_ld_u32x4(part + t * kTileM + 4 * lane, (uint32_t)j);
+      v[0] += __uint_as_float(q.x);
+      v[1] += __uint_as_float(q.y);
+      v[2] += __uint_as_float(q.z);
+      v[3] += __uint_as_float(q.w);
+    }
+    const int64_t at = (m0 + t) * p.y_ld + (int64_t)z * p.y_noff + n0 + 4 * lane;
+    if constexpr (OUT == kFp8Out) {   // N is a multiple of 128
+      float am = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+      am = warp_max(am);
+      if (isinf(am)) {   // warp-uniform
+        am = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = fmaxf(am, isinf(v[i]) ? 0.f : fabsf(v[i]));
+        am = warp_max(am);
+      }
+      const uint32_t byte = scale_byte(am);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + at) = codes4(v, byte);
+      if (lane == 0) p.y_sf[at / 128] = (uint8_t)byte;
+    } else {
+      const int n = p.N - n0 - 4 * lane;   // columns of Y from this lane's first on
+      if (OUT == CSA_BF16) {
+        bf16* dst = static_cast<bf16*>(p.y) + at;
+        if (a.vec && n >= 4) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]),
+                                                      pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+        }
+      } else {
+        float* dst = static_cast<float*>(p.y) + at;
+        if (a.vec && n >= 4) {
+          store_vec(dst, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < n) dst[i] = v[i];
+        }
+      }
+    }
+  }
+  if (split > 1) cluster_sync();   // the others have read this CTA's partials
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::cols);
+  }
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 148;
+  return n;
+}
+
+template <int OUT>
+cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
+  const Fp8GemmParams& p = a.p;
+  a.m_tiles = (int)((p.M + kTileM - 1) / kTileM);
+  a.n_tiles = (p.N + kN - 1) / kN;
+  a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
+  CUtensorMap mx, mw;
+  if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, kTileM) ||
+      !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kN))
+    return cudaErrorInvalidValue;
+  const int smem = kSmem + 1024;
+  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<OUT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t sms = sm_count();
+  const unsigned grid = (unsigned)(a.tiles < sms ? a.tiles : sms);
+  return launch_pdl(fp8_gemm_kernel<OUT>, dim3(grid), dim3(kThreads), smem, stream, mx, mw, a);
+}
+
+template <int NT, int OUT>
+cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
+  using L = Few<NT>;
+  const Fp8GemmParams& p = a.p;
+  a.m_tiles = (int)((p.M + NT - 1) / NT);
+  a.n_tiles = (p.N + kTileM - 1) / kTileM;
+  a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
+  // K shares: as many as keep two CTAs on every SM at once
+  const int chunks = (a.kb_n + kChunk - 1) / kChunk;
+  const int64_t room = 2 * sm_count();
+  int split = 1;
+  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room) split *= 2;
+  if (a.tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  CUtensorMap mx, mw;
+  if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, NT) ||
+      !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kTileM))
+    return cudaErrorInvalidValue;
+  const int smem = L::smem + 1024;
+  auto kernel = fp8_gemm_few_kernel<NT, OUT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.tiles * split));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a, split);
+}
+
+template <int OUT>
+cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
+  const Fp8GemmParams& p = a.p;
+  const int64_t tiles = (int64_t)p.Z * ((p.M + kTileM - 1) / kTileM) * ((p.N + kN - 1) / kN);
+  if (p.M > 128 && tiles >= 96) return launch_many<OUT>(a, stream);
+  if (p.M <= 16) return launch_few<16, OUT>(a, stream);
+  if (p.M <= 32) return launch_few<32, OUT>(a, stream);
+  if (p.M <= 64) return launch_few<64, OUT>(a, stream);
+  return launch_few<128, OUT>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream) {
   if (p.M == 0 || p.N == 0) return cudaSuccess;
-  const dim3 grid((unsigned)((p.M + kT - 1) / kT), (unsigned)((p.N + kT - 1) / kT), (unsigned)p.Z);
-  return launch_pdl(fp8_gemm_kernel, grid, dim3(256), 0, stream, p);
+  GemmArgs a{};
+  a.p = p;
+  a.kb_n = (p.K + kBK - 1) / kBK;
+  a.x_blocks = (p.x_cols + 127) / 128;
+  a.w_rblocks = (p.N + 127) / 128;
+  a.x_words = a.x_blocks % kChunk == 0 && p.x_koff / 128 % kChunk == 0 &&
+              (reinterpret_cast<uintptr_t>(p.x_sf) & 3u) == 0;
+  a.w_words = a.kb_n % kChunk == 0 && (reinterpret_cast<uintptr_t>(p.w_sf) & 3u) == 0;
+  const int64_t e = p.out == CSA_BF16 ? 2 : 4;
+  a.vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_ld * e % 16 == 0;
+  switch (p.out) {
+    case CSA_BF16: return launch<CSA_BF16>(a, stream);
+    case CSA_F32: return launch<CSA_F32>(a, stream);
+    default: return launch<kFp8Out>(a, stream);
+  }
 }
 
 }  // namespace csa

@@ -83,7 +83,7 @@ def proj(L, dtype=BF16, T=4, H=8, c=64, g=2, dg=128, d=96, o=PTR, wg=PTR, wgs=PT
     (dict(dtype=9), ARG), (dict(T=-1), ARG), (dict(H=0), ARG), (dict(g=0), ARG), (dict(d=0), ARG),
     (dict(o=None), ARG), (dict(wgs=None), ARG), (dict(wos=None), ARG), (dict(y=MIS), ARG),
     (dict(wg=MIS), ARG), (dict(g=3), UNSUPPORTED), (dict(g=8), UNSUPPORTED),
-    (dict(dg=96), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=4096), WORKSPACE),
+    (dict(dg=96), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws_bytes=3000), WORKSPACE),
     (dict(ws=MIS), WORKSPACE), (dict(T=0), 0),
 ])
 def test_projection_refusals(L, change, want):
