@@ -435,61 +435,67 @@ def grouped_output_projection(o, w_group, w_out, y=None, ws=None, stream=None):
 
 
 
+# The calls below may follow one another every few microseconds (one token's
+# norm and projections), so their checks build no message unless they fail.
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_FP8_TYPES = (_E4M3, _E8M0, torch.uint8)
+
+
 def _launch(dev, stream, what, fn, *args):
     """fn(*args, stream) on `dev`'s current stream unless one is given, with
     `dev` current while it launches."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
+    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+           else stream.cuda_stream)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, raw)
     if st != CSA_OK:
         raise CSAError(st, what)
 
 
-def _arg(ok, what: str):
-    if not ok:
-        raise CSAError(CSA_E_ARG, what)
+def _refuse(what: str):
+    raise CSAError(CSA_E_ARG, what)
 
 
 def _fp8(t, shape, dev, what: str):
     """Address of contiguous FP8 codes or scales of the given shape on dev."""
-    _arg(t.dtype in (torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu), f"{what}: dtype")
-    _arg(tuple(t.shape) == shape, f"{what}: shape {tuple(t.shape)}, expected {shape}")
-    _arg(t.is_contiguous() and t.device == dev, f"{what}: contiguous, on {dev}")
+    if (t.dtype not in _FP8_TYPES or t.shape != shape or t.device != dev
+            or not t.is_contiguous()):
+        _refuse(f"{what}: contiguous FP8 of shape {tuple(shape)} on {dev} expected, got "
+                f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, d: int, dev, dtype, what: str):
-    """(rows, row stride) of a [..., d] tensor: contiguous, or two-dimensional
-    with contiguous rows."""
-    _arg(t.dtype == dtype and t.device == dev, f"{what}: dtype {dtype} on {dev}")
-    _arg(t.dim() >= 1 and t.shape[-1] == d, f"{what}: last dim {d}")
+def _row_stride(t, shape, dtype, dev, what: str):
+    """Row stride of a [..., d] tensor: contiguous, or two-dimensional with
+    contiguous rows."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev:
+        _refuse(f"{what}: {dtype} of shape {tuple(shape)} on {dev} expected, got {t.dtype} "
+                f"{tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
-        return t.numel() // d, d
-    _arg(t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= d,
-         f"{what}: contiguous, or two-dimensional with contiguous rows")
-    return t.shape[0], t.stride(0)
+        return shape[-1]
+    if len(shape) != 2 or t.stride(1) != 1 or t.stride(0) < shape[1]:
+        _refuse(f"{what}: contiguous, or two-dimensional with contiguous rows")
+    return t.stride(0)
 
 
-def _fp8_out(rows_shape, d: int, dev, codes, scales, block_rows=1):
-    """Code and scale outputs ([rows..., d], [row blocks..., ceil(d / 128)])."""
-    nb = (d + 127) // 128
-    cs = tuple(rows_shape) + (d,)
-    ss = (tuple(rows_shape) if block_rows == 1
-          else ((rows_shape[0] + 127) // 128,)) + (nb,)
-    if codes is None:
-        codes = torch.empty(cs, dtype=torch.float8_e4m3fn, device=dev)
-    if scales is None:
-        scales = torch.empty(ss, dtype=torch.float8_e8m0fnu, device=dev)
-    return codes, scales, _fp8(codes, cs, dev, "codes"), _fp8(scales, ss, dev, "scales")
+def _cuda_rows(x, what: str):
+    """Device of a CUDA tensor [..., d] with d > 0."""
+    if not x.is_cuda or x.dim() < 1 or x.shape[-1] < 1:
+        _refuse(f"{what}: a CUDA tensor [..., d]")
+    return x.device
 
 
-def _cuda(t, what: str):
-    _arg(t.is_cuda, f"{what}: tensors must live on a CUDA device")
-    return t.device
+def _ws(ws, nbytes: int, dev):
+    """The workspace given, checked, or one of the call's own."""
+    if ws is None:
+        return workspace(nbytes, dev)
+    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
+        _refuse(f"ws: contiguous uint8 on {dev}")
+    return ws
 
 
 def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, codes=None,
@@ -498,44 +504,59 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
     activations: codes [..., d] float8_e4m3fn and scales [..., ceil(d/128)]
     float8_e8m0fnu.  With a residual also returns x + residual (in ``sum_out``,
     which may be x or residual itself)."""
-    dev = _cuda(x, "rmsnorm_fp8")
-    dt = _dt(x)
-    _arg(x.dim() >= 1 and x.shape[-1] > 0, "x: [..., d]")
-    d = x.shape[-1]
-    T, x_ld = _rows(x, d, dev, x.dtype, "x")
+    dev = _cuda_rows(x, "rmsnorm_fp8")
+    dt, shape = x.dtype, x.shape
+    d = shape[-1]
+    x_ld = _row_stride(x, shape, dt, dev, "x")
+    sshape = shape[:-1] + ((d + 127) // 128,)
     r_ld = s_ld = 0
+    pr = ps = pg = None
     if residual is not None:
-        _arg(residual.shape == x.shape, "residual: x's shape")
-        r_ld = _rows(residual, d, dev, x.dtype, "residual")[1]
+        r_ld = _row_stride(residual, shape, dt, dev, "residual")
+        pr = residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        _arg(sum_out.shape == x.shape, "sum_out: x's shape")
-        s_ld = _rows(sum_out, d, dev, x.dtype, "sum_out")[1]
-    else:
-        _arg(sum_out is None, "sum_out needs a residual")
+            sum_out = torch.empty(shape, dtype=dt, device=dev)
+            s_ld = d
+        else:
+            s_ld = _row_stride(sum_out, shape, dt, dev, "sum_out")
+        ps = sum_out.data_ptr()
+    elif sum_out is not None:
+        _refuse("sum_out needs a residual")
     if gain is not None:
-        _arg(gain.dtype == torch.float32 and tuple(gain.shape) == (d,) and gain.is_contiguous()
-             and gain.device == dev, "gain: [d] float32")
-    codes, scales, pc, ps = _fp8_out(x.shape[:-1], d, dev, codes, scales)
-    _launch(dev, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, dt, T, d, x.data_ptr(), x_ld,
-            None if residual is None else residual.data_ptr(), r_ld,
-            None if gain is None else gain.data_ptr(), eps,
-            None if sum_out is None else sum_out.data_ptr(), s_ld, pc, ps)
+        if (gain.dtype != torch.float32 or gain.shape != (d,) or gain.device != dev
+                or not gain.is_contiguous()):
+            _refuse("gain: contiguous [d] float32")
+        pg = gain.data_ptr()
+    if codes is None:
+        codes = torch.empty(shape, dtype=_E4M3, device=dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=_E8M0, device=dev)
+    _launch(dev, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, _dt(x), x.numel() // d, d,
+            x.data_ptr(), x_ld, pr, r_ld, pg, eps, ps, s_ld, _fp8(codes, shape, dev, "codes"),
+            _fp8(scales, sshape, dev, "scales"))
     return (codes, scales) if sum_out is None else (codes, scales, sum_out)
 
 
 def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
     """FP8 activations of x [..., d] (block_rows 1), or FP8 weights of x
     [rows, d] (block_rows 128): codes and scales [ceil(rows/128), ceil(d/128)]."""
-    dev = _cuda(x, "fp8_quantize")
-    dt = _dt(x)
-    _arg(x.dim() >= 1 and x.shape[-1] > 0, "x: [..., d]")
-    _arg(block_rows == 1 or x.dim() == 2, "weights: [rows, d]")
-    d = x.shape[-1]
-    rows, ld = _rows(x, d, dev, x.dtype, "x")
-    codes, scales, pc, ps = _fp8_out(x.shape[:-1], d, dev, codes, scales, block_rows)
-    _launch(dev, stream, "fp8_quantize", lib().fp8_quantize, dt, rows, d, x.data_ptr(), ld,
-            block_rows, pc, ps)
+    dev = _cuda_rows(x, "fp8_quantize")
+    shape = x.shape
+    d = shape[-1]
+    ld = _row_stride(x, shape, x.dtype, dev, "x")
+    if block_rows == 1:
+        sshape = shape[:-1] + ((d + 127) // 128,)
+    elif x.dim() == 2:
+        sshape = ((shape[0] + 127) // 128, (d + 127) // 128)
+    else:
+        _refuse("fp8_quantize: weights are [rows, d]")
+    if codes is None:
+        codes = torch.empty(shape, dtype=_E4M3, device=dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=_E8M0, device=dev)
+    _launch(dev, stream, "fp8_quantize", lib().fp8_quantize, _dt(x), x.numel() // d, d,
+            x.data_ptr(), ld, block_rows, _fp8(codes, shape, dev, "codes"),
+            _fp8(scales, sshape, dev, "scales"))
     return codes, scales
 
 
@@ -544,31 +565,26 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
     """y = x w^T of FP8 activations (codes [..., K], scales [..., ceil(K/128)])
     and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
     bf16 or fp32.  ``y`` may be a two-dimensional column slice of a wider buffer."""
-    dev = _cuda(x_codes, "fp8_matmul")
-    _arg(x_codes.dim() >= 1 and w_codes.dim() == 2, "x_codes: [..., K], w_codes: [N, K]")
-    lead, K = tuple(x_codes.shape[:-1]), x_codes.shape[-1]
-    N, nb = w_codes.shape[0], (K + 127) // 128
-    px = _fp8(x_codes, lead + (K,), dev, "x_codes")
-    pxs = _fp8(x_scales, lead + (nb,), dev, "x_scales")
-    pw = _fp8(w_codes, (N, K), dev, "w_codes")
-    pws = _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales")
+    dev = _cuda_rows(x_codes, "fp8_matmul")
+    shape = x_codes.shape
+    K, nb = shape[-1], (shape[-1] + 127) // 128
+    if w_codes.dim() != 2:
+        _refuse("w_codes: [N, K]")
+    N = w_codes.shape[0]
+    yshape = shape[:-1] + (N,)
     if y is None:
-        y = torch.empty(lead + (N,), dtype=out_dtype, device=dev)
-    _arg(tuple(y.shape) == lead + (N,), f"y: shape {lead + (N,)}")
-    M = 1
-    for n in lead:
-        M *= n
-    y_ld = _rows(y, N, dev, y.dtype, "y")[1] if N else 0
-    if ws is None:
-        ws = workspace(256, dev)
-    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), M, N, K, px, pxs, pw, pws,
-            y.data_ptr(), y_ld, _ws(ws, dev), ws.numel())
+        y = torch.empty(yshape, dtype=out_dtype, device=dev)
+        y_ld = N
+    else:
+        y_ld = _row_stride(y, yshape, y.dtype, dev, "y")
+    ws = _ws(ws, 256, dev)
+    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), x_codes.numel() // K, N, K,
+            _fp8(x_codes, shape, dev, "x_codes"),
+            _fp8(x_scales, shape[:-1] + (nb,), dev, "x_scales"),
+            _fp8(w_codes, (N, K), dev, "w_codes"),
+            _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales"), y.data_ptr(), y_ld,
+            ws.data_ptr(), ws.numel())
     return y
-
-
-def _ws(ws, dev):
-    _arg(ws.dtype == torch.uint8 and ws.device == dev and ws.is_contiguous(), f"ws: uint8 on {dev}")
-    return ws.data_ptr()
 
 
 def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scales, y=None,
@@ -576,27 +592,29 @@ def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scale
     """Grouped output projection in FP8: o [T, H, c] (bf16 or fp32), w_group
     [g, d_g, (H/g) c] and w_out [d, g d_g] FP8 weights (the scales of w_group
     [g, d_g/128, (H/g) c/128]) -> y [T, d] bf16."""
-    dev = _cuda(o, "grouped_output_projection_fp8")
-    _arg(o.dim() == 3 and w_group.dim() == 3 and w_out.dim() == 2,
-         "o: [T, H, c], w_group: [g, d_g, k], w_out: [d, g d_g]")
+    dev = _cuda_rows(o, "grouped_output_projection_fp8")
+    if o.dim() != 3 or w_group.dim() != 3 or w_out.dim() != 2 or not o.is_contiguous():
+        _refuse("o: contiguous [T, H, c], w_group: [g, d_g, k], w_out: [d, g d_g]")
     T, H, c = o.shape
     g, dg, kg = w_group.shape
     d = w_out.shape[0]
-    _arg(o.is_contiguous() and g * kg == H * c, "o: contiguous, H c = g k")
-    if kg % 128 or dg % 128:
-        raise CSAError(CSA_E_UNSUPPORTED, "grouped_output_projection_fp8: (H/g) c and d_g are "
-                       "multiples of 128")
-    pg = _fp8(w_group, (g, dg, kg), dev, "w_group")
-    pgs = _fp8(w_group_scales, (g, dg // 128, kg // 128), dev, "w_group_scales")
-    po = _fp8(w_out, (d, g * dg), dev, "w_out")
-    pos = _fp8(w_out_scales, ((d + 127) // 128, g * dg // 128), dev, "w_out_scales")
+    if g * kg != H * c:
+        _refuse("w_group: [g, d_g, (H/g) c]")
+    if H % g or kg % 128 or dg % 128:
+        raise CSAError(CSA_E_UNSUPPORTED, "grouped_output_projection_fp8: g divides H, (H/g) c "
+                       "and d_g are multiples of 128")
     if y is None:
         y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    _arg(tuple(y.shape) == (T, d) and y.dtype == torch.bfloat16 and y.is_contiguous()
-         and y.device == dev, "y: [T, d] bf16")
+    elif _row_stride(y, (T, d), torch.bfloat16, dev, "y") != d:
+        _refuse("y: contiguous")
     if ws is None:
         ws = workspace(csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, _dt(o), 1, T, H, c, g * dg), dev)
+    else:
+        ws = _ws(ws, 0, dev)
     _launch(dev, stream, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
-            _dt(o), T, H, c, g, dg, d, o.data_ptr(), pg, pgs, po, pos, y.data_ptr(),
-            _ws(ws, dev), ws.numel())
+            _dt(o), T, H, c, g, dg, d, o.data_ptr(), _fp8(w_group, (g, dg, kg), dev, "w_group"),
+            _fp8(w_group_scales, (g, dg // 128, kg // 128), dev, "w_group_scales"),
+            _fp8(w_out, (d, g * dg), dev, "w_out"),
+            _fp8(w_out_scales, ((d + 127) // 128, g * dg // 128), dev, "w_out_scales"),
+            y.data_ptr(), ws.data_ptr(), ws.numel())
     return y

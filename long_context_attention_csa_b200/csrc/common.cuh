@@ -104,6 +104,14 @@ __device__ __forceinline__ void store_vec(bf16* p, const float* v) {
   *reinterpret_cast<uint4*>(p) = u;
 }
 
+// One 32-byte sector in one store (32-byte aligned): a lane that writes a row of
+// its own then leaves no half sector for the L2 to merge.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
 

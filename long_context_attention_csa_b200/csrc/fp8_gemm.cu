@@ -37,10 +37,12 @@ constexpr int kChunk = 4;         // scale blocks per TMEM word
 constexpr int kTileM = 128;       // MMA M
 constexpr int kTileA = kTileM * kBK;
 
-// Scale bytes 4 c .. 4 c + 3 of a row of scales: block b's byte in byte b mod 4.
-// Bytes at or past `end` (the row's blocks) are not read.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int b0, int end, bool words) {
-  if (words) return *reinterpret_cast<const uint32_t*>(row + b0);
+// Scale bytes b0 .. b0 + 3 of a row of `end` scales, block b's in byte b - b0.
+// Bytes at or past `end` are not read (0).  `align`: the row starts, and b0 and
+// `end` lie, on multiples of that many bytes.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int b0, int end, int align) {
+  if (b0 >= end) return 0;
+  if (align >= 4) return *reinterpret_cast<const uint32_t*>(row + b0);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < kChunk; ++i)
@@ -48,13 +50,26 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int b0, int e
   return w;
 }
 
+// Four consecutive scale words.
+__device__ __forceinline__ void scale_words(const uint8_t* row, int b0, int end, int align,
+                                            uint32_t* w) {
+  if (align >= 16) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (b0 < end) q = *reinterpret_cast<const uint4*>(row + b0);
+    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = scale_word(row, b0 + c * kChunk, end, align);
+  }
+}
+
 struct GemmArgs {
   Fp8GemmParams p;
   int kb_n;              // scale blocks (stages) of K
   int x_blocks;          // scale blocks of a row of X
   int w_rblocks;         // scale block rows of one W
-  bool x_words, w_words; // scale rows start on 4-byte boundaries and end on them
-  bool vec;              // rows of Y start on 16-byte boundaries
+  int x_align, w_align;  // 16, 4 or 1: what scale rows and the groups' first blocks lie on
+  int y_align;           // 32, 16 or 1: the boundaries that rows of Y start on
   int64_t tiles;
   int m_tiles, n_tiles;
 };
@@ -72,26 +87,28 @@ __device__ __forceinline__ void store_codes128(const float* v, uint8_t* codes, u
   const uint32_t byte = scale_byte(a);
   *scale = (uint8_t)byte;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const uint2 lo = codes8(v + 16 * q, byte), hi = codes8(v + 16 * q + 8, byte);
-    reinterpret_cast<uint4*>(codes)[q] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = codes4(v + 32 * q + 4 * i, byte);
+    store_sector(codes + 32 * q, w);
   }
 }
 
-// Thirty-two consecutive values of one row, `n` of them inside Y.
+// Thirty-two consecutive values of one row, `n` of them inside Y.  `sectors`:
+// rows of Y start on 32-byte boundaries.
 template <int OUT>
 __device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r, int n,
-                                            bool vec) {
+                                            bool sectors) {
   if constexpr (OUT == CSA_BF16) {
     bf16* dst = static_cast<bf16*>(y) + at;
-    if (vec && n >= 32) {
+    if (sectors && n >= 32) {
+      uint32_t w[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        reinterpret_cast<uint4*>(dst)[q] = make_uint4(
-            pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
-            pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
-            pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
-            pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      store_sector(dst, w);
+      store_sector(dst + 16, w + 8);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -99,11 +116,9 @@ __device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t*
     }
   } else {
     float* dst = static_cast<float*>(y) + at;
-    if (vec && n >= 32) {
+    if (sectors && n >= 32) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        reinterpret_cast<uint4*>(dst)[q] =
-            make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+      for (int q = 0; q < 4; ++q) store_sector(dst + 8 * q, r + 8 * q);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -114,26 +129,33 @@ __device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t*
 
 // ---- many rows ----------------------------------------------------------------
 //
-// Persistent CTAs walk 128 x 256 tiles, n fastest (the CTAs that run at once
-// share their X tiles and all of W through L2).
-//   warp 0     TMA producer, a four-slot ring of K blocks (16 + 32 KB)
-//   warp 1     TMEM owner, single-thread MMA issuer
-//   warp 2     scale tiles
+// Persistent CTA pairs walk 256 x 256 tiles, n fastest (the pairs that run at
+// once share their X tiles and all of W through L2).  One MMA spans the pair
+// (cta_group::2): each CTA holds 128 rows of X and of the accumulator and half
+// of the tile's W, so an SM reads 32 KB per K block instead of the 48 KB of a
+// 128 x 256 tile of its own.
+//   warp 0     TMA producer, a six-slot ring of K blocks (16 + 16 KB); both CTAs'
+//              loads complete on rank 0's barrier
+//   warp 1     TMEM owner; rank 0: single-thread MMA issuer for the pair
+//   warp 2     scale tiles in shared memory
 //   warps 4-7  epilogue, thread = row
 // The two 256-column accumulators and the scales' 24 columns do not fit 512, so
 // the accumulators share 24 columns: the epilogue reads those first and only
 // then lets the next tile's MMAs begin.
 constexpr int kN = 256;
-constexpr int kStages = 4;
-constexpr int kStage = kTileA + kN * kBK;
+constexpr int kStages = 6;
+constexpr int kStage = kTileA + kN / 2 * kBK;   // bytes of one CTA
 constexpr int kSfSlot = 512 + kN / 128 * 512;
 constexpr int kOffSf = kStages * kStage;
-constexpr int kOffBar = kOffSf + 2 * kSfSlot;
+constexpr int kGroup = 4;                       // chunks whose scales are handed over together
+constexpr int kSfSlots = 3;                     // such groups in shared memory
+constexpr int kOffBar = kOffSf + kSfSlots * kGroup * kSfSlot;
 constexpr int kSmem = kOffBar + 256;
 constexpr int kThreads = 256;
 constexpr uint32_t kAcc1 = 232;               // second accumulator: columns 232 .. 487
 constexpr uint32_t kSfCol = 488;              // scales: 2 x (4 + 8) columns
 static_assert(kSmem + 1024 <= 232448, "shared memory budget");
+static_assert(kGroup == 4, "scale_words loads four");
 
 template <int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -141,16 +163,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap map_w, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kOffBar);   // [stages] operands landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + kOffBar);   // [stages] operands landed (rank 0)
   uint64_t* empty = full + kStages;         // [stages] operands consumed
-  uint64_t* sfull = empty + kStages;        // [2] scale tiles written
-  uint64_t* sempty = sfull + 2;             // [2] the chunk's MMAs are done
-  uint64_t* tfull = sempty + 2;             // accumulator complete
-  uint64_t* tfree = tfull + 1;              // the shared columns have been read
+  uint64_t* sfull = empty + kStages;        // [slots] both CTAs' scale tiles written (rank 0)
+  uint64_t* sempty = sfull + kSfSlots;      // [slots] the group's MMAs are done
+  uint64_t* cdone = sempty + kSfSlots;      // [2] the chunk's MMAs are done (rank 0)
+  uint64_t* tfull = cdone + 2;              // accumulator complete
+  uint64_t* tfree = tfull + 1;              // the shared columns have been read (rank 0)
   uint64_t* drain = tfree + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const Fp8GemmParams& p = a.p;
 
   if (threadIdx.x == 0) {
@@ -158,12 +183,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sfull[s], 1);
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sfull[s], 2);
       mbar_init(&sempty[s], 1);
     }
+    mbar_init(&cdone[0], 1);
+    mbar_init(&cdone[1], 1);
     mbar_init(tfull, 1);
-    mbar_init(tfree, 128);
+    mbar_init(tfree, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -171,11 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&map_w);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -184,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile_of = [&](int64_t u, int& z, int64_t& m0, int& n0) {
     const int nt = (int)(u % a.n_tiles);
     const int64_t r = u / a.n_tiles;
-    m0 = (r % a.m_tiles) * kTileM;
+    m0 = (r % a.m_tiles) * (2 * kTileM) + rank * kTileM;   // this CTA's rows
     z = (int)(r / a.m_tiles);
     n0 = nt * kN;
   };
@@ -196,123 +224,157 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       uint32_t it = 0;
-      for (int64_t u = blockIdx.x; u < a.tiles && !*abort_flag; u += gridDim.x) {
+      bool ok = true;
+      for (int64_t u = first; u < a.tiles && ok; u += step) {
         int z, n0;
         int64_t m0;
         tile_of(u, z, m0, n0);
         for (int kb = 0; kb < a.kb_n; ++kb) {
           const uint32_t s = it % kStages;
-          if (*abort_flag || !mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u)) {
+          ok = !*abort_flag && mbar_wait(&empty[s], ((it / kStages) & 1u) ^ 1u);
+          if (!ok) {
             give_up(0x801u);
             break;
           }
-          mbar_arrive_expect_tx(&full[s], kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          const uint32_t bar = cluster_addr(&full[s], 0);
           uint8_t* dst = sm + s * kStage;
-          tma_load_3d(dst, &map_x, &full[s], z * p.x_koff + kb * kBK, (int32_t)m0, 0);
-          tma_load_3d(dst + kTileA, &map_w, &full[s], kb * kBK, n0, z);
+          tma_load_3d_pair(dst, &map_x, bar, z * p.x_koff + kb * kBK, (int32_t)m0, 0);
+          tma_load_3d_pair(dst + kTileA, &map_w, bar, kb * kBK,
+                           n0 + (int)rank * (kN / 2), z);
           ++it;
         }
       }
-      // every issued copy has landed before the CTA may exit
-      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-        mbar_wait(&full[i % kStages], (i / kStages) & 1u);
+      // rank 0's commits have all arrived here before this CTA may exit, which
+      // also says that every load has landed; after a timeout the loads in
+      // flight are given a millisecond
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it && ok; ++i)
+        ok = mbar_wait(&empty[i % kStages], (i / kStages) & 1u);
+      if (!ok)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {
+        }
     }
   } else if (warp == 1) {
-    if (elect_one()) {
-      uint32_t it = 0, ch = 0, n = 0;
-      for (int64_t u = blockIdx.x; u < a.tiles; u += gridDim.x, ++n) {
-        if (*abort_flag || (n > 0 && !mbar_wait(tfree, (n - 1) & 1u))) {
+    if (rank == 0 && elect_one()) {
+      uint32_t it = 0, ch = 0, gr = 0, n = 0;   // stages, chunks, groups, tiles
+      bool landed = false;                      // stage `it` is known to have landed
+      for (int64_t u = first; u < a.tiles; u += step, ++n) {
+        if (*abort_flag || (n > 0 && !mbar_wait_cluster(tfree, (n - 1) & 1u))) {
           give_up(0x802u);
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + ((n & 1u) ? kAcc1 : 0u);
         bool ok = true;
-        for (int kb = 0; kb < a.kb_n && ok; ++kb, ++it) {
-          const uint32_t s = it % kStages, slot = ch & 1u;
-          const uint32_t sfa = tmem + kSfCol + slot * 12u, sfb = sfa + 4u;
-          if ((kb & 3) == 0) {
-            ok = !*abort_flag && mbar_wait(&sfull[slot], (ch >> 1) & 1u);
+        for (int kb = 0; kb < a.kb_n; ++kb, ++it) {
+          const uint32_t s = it % kStages, slot = gr % kSfSlots;
+          const uint32_t sfa = tmem + kSfCol + (ch & 1u) * 12u, sfb = sfa + 4u;
+          const int c = kb / kChunk % kGroup;   // chunk of its group
+          ok = !*abort_flag;
+          if (ok && kb % kChunk == 0) {
+            // the MMAs of the chunk before last are done with these columns
+            ok = (ch < 2 || mbar_wait(&cdone[ch & 1u], ((ch >> 1) - 1) & 1u)) &&
+                 (c != 0 || mbar_wait_cluster(&sfull[slot], (gr / kSfSlots) & 1u));
             if (ok) {
               tc_fence_after();
-              const uint32_t ss = smem_u32(sm + kOffSf + slot * kSfSlot);
-              tmem_cp_32x128b_x4(sfa, smem_desc(ss, 16, 128, 0));
-              tmem_cp_32x128b_x4(sfb, smem_desc(ss + 512, 16, 128, 0));
-              tmem_cp_32x128b_x4(sfb + 4, smem_desc(ss + 1024, 16, 128, 0));
+              const uint32_t ss = smem_u32(sm + kOffSf + (slot * kGroup + c) * kSfSlot);
+              tmem_cp_32x128b_x4_pair(sfa, smem_desc(ss, 16, 128, 0));
+              tmem_cp_32x128b_x4_pair(sfb, smem_desc(ss + 512, 16, 128, 0));
+              tmem_cp_32x128b_x4_pair(sfb + 4, smem_desc(ss + 1024, 16, 128, 0));
             }
           }
-          ok = ok && !*abort_flag && mbar_wait(&full[s], (it / kStages) & 1u);
+          ok = ok && (landed || mbar_wait(&full[s], (it / kStages) & 1u));
           if (!ok) {
             give_up(0x803u);
             break;
           }
           tc_fence_after();
+          // Issuing four MMAs takes this thread about 340 of the 512 cycles that
+          // they run for, so it looks at the next stage's barrier before it does.
+          landed = mbar_test(&full[(it + 1) % kStages], ((it + 1) / kStages) & 1u);
           const uint32_t sa = smem_u32(sm + s * kStage);
           const uint32_t id = (uint32_t)kb & 3u;
-          const uint32_t idesc = idesc_mxf8_e4m3(kTileM, kN, id, id);
+          const uint32_t idesc = idesc_mxf8_e4m3(2 * kTileM, kN, id, id);
 #pragma unroll
           for (int kk = 0; kk < kBK / 32; ++kk)
-            mma_mxf8_ss(d, smem_desc(sa + kk * 32, 16, 1024, 2),
-                        smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc, sfa | (id << 30),
-                        sfb | (id << 30), (kb > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&empty[s]);
-          if ((kb & 3) == 3 || kb == a.kb_n - 1) {
-            mma_commit(&sempty[slot]);
+            mma_mxf8_ss_pair(d, smem_desc(sa + kk * 32, 16, 1024, 2),
+                             smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc,
+                             sfa | (id << 30), sfb | (id << 30), (kb > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_pair(&empty[s]);
+          const bool last = kb == a.kb_n - 1;
+          if (kb % kChunk == kChunk - 1 || last) {
+            mma_commit_one_of_pair(&cdone[ch & 1u]);
             ++ch;
+            if (c == kGroup - 1 || last) {
+              mma_commit_pair(&sempty[slot]);
+              ++gr;
+            }
           }
         }
         if (!ok) break;
-        mma_commit(tfull);
+        mma_commit_pair(tfull);
       }
-      mma_commit(drain);
-      mbar_wait(drain, 0);
+      mma_commit_pair(drain);
     }
+    __syncwarp();
+    mbar_wait(drain, 0);
   } else if (warp == 2) {
     // scale tiles: a lane holds rows lane, lane + 32, ... of X; W's rows all
-    // carry their 128-row block's word
-    uint32_t ch = 0;
+    // carry their 128-row block's word.  The fence and the arrival at rank 0
+    // take about as long as a chunk's MMAs (2400 of 2048 cycles), so four chunks
+    // are handed over at once: 281 -> 253 us for 9472 x 2048 x 16384 with the
+    // loads grouped alone.
+    uint32_t gr = 0;
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < a.tiles && ok; u += gridDim.x) {
+    for (int64_t u = first; u < a.tiles && ok; u += step) {
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
       const int xb0 = z * (p.x_koff / 128);
       const uint8_t* wrow = p.w_sf + ((int64_t)z * a.w_rblocks + n0 / 128) * a.kb_n;
-      const bool second = n0 / 128 + 1 < a.w_rblocks;
-      auto load = [&](int kb, uint32_t* x, uint32_t* w) {
+      const int wend1 = n0 / 128 + 1 < a.w_rblocks ? a.kb_n : 0;
+      for (int kb = 0; kb < a.kb_n; kb += kGroup * kChunk, ++gr) {
+        uint32_t x[4][kGroup], w[2][kGroup];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t m = m0 + 32 * i + lane;
-          x[i] = m < p.M ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_words)
-                         : 0u;
+          scale_words(p.x_sf + m * a.x_blocks, xb0 + kb, m < p.M ? a.x_blocks : 0, a.x_align,
+                      x[i]);
         }
-        w[0] = scale_word(wrow, kb, a.kb_n, a.w_words);
-        w[1] = second ? scale_word(wrow + a.kb_n, kb, a.kb_n, a.w_words) : 0u;
-      };
-      uint32_t x[4], w[2];
-      load(0, x, w);
-      for (int kb = 0; kb < a.kb_n; kb += kChunk, ++ch) {
-        const uint32_t slot = ch & 1u;
-        ok = __all_sync(0xffffffffu,
-                        !*abort_flag && mbar_wait(&sempty[slot], ((ch >> 1) & 1u) ^ 1u));
+        scale_words(wrow, kb, a.kb_n, a.w_align, w[0]);
+        scale_words(wrow + a.kb_n, kb, wend1, a.w_align, w[1]);
+        const uint32_t slot = gr % kSfSlots;
+        ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[slot],
+                                                               ((gr / kSfSlots) & 1u) ^ 1u));
         if (!ok) {
           give_up(0x804u);
           break;
         }
-        uint4* dst = reinterpret_cast<uint4*>(sm + kOffSf + slot * kSfSlot) + lane;
-        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        dst[32] = make_uint4(w[0], w[0], w[0], w[0]);
-        dst[64] = make_uint4(w[1], w[1], w[1], w[1]);
-        fence_proxy_async_smem();
+#pragma unroll
+        for (int c = 0; c < kGroup; ++c) {
+          uint4* dst =
+              reinterpret_cast<uint4*>(sm + kOffSf + (slot * kGroup + c) * kSfSlot) + lane;
+          dst[0] = make_uint4(x[0][c], x[1][c], x[2][c], x[3][c]);
+          dst[32] = make_uint4(w[0][c], w[0][c], w[0][c], w[0][c]);
+          dst[64] = make_uint4(w[1][c], w[1][c], w[1][c], w[1][c]);
+        }
+        fence_proxy_async_all();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[slot]);
-        if (kb + kChunk < a.kb_n) load(kb + kChunk, x, w);
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&sfull[slot], 0));
       }
     }
+    for (uint32_t i = gr > kSfSlots ? gr - kSfSlots : 0; i < gr && ok; ++i)   // the last commits
+      ok = mbar_wait(&sempty[i % kSfSlots], (i / kSfSlots) & 1u);
   } else if (warp >= 4) {
     const int quarter = warp & 3;
+    const uint32_t free_bar = cluster_addr(tfree, 0);
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(free_bar);
+    };
     uint32_t n = 0;
-    for (int64_t u = blockIdx.x; u < a.tiles; u += gridDim.x, ++n) {
+    for (int64_t u = first; u < a.tiles; u += step, ++n) {
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
@@ -335,10 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(base + h * 128 + q * 32, r + q * 32);
           tmem_ld_wait();
-          if (i == 0) {
-            tc_fence_before();
-            mbar_arrive(tfree);
-          }
+          if (i == 0) release();
           if (live && n0 + h * 128 < p.N)   // N is a multiple of 128
             store_codes128(reinterpret_cast<const float*>(r),
                            static_cast<uint8_t*>(p.y) + at + h * 128,
@@ -351,11 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32];
           tmem_ld32(base + cc, r);
           tmem_ld_wait();
-          if (i == 0) {
-            tc_fence_before();
-            mbar_arrive(tfree);
-          }
-          if (live && n0 + cc < p.N) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.vec);
+          if (i == 0) release();
+          if (live && n0 + cc < p.N) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.y_align >= 32);
         }
       }
     }
@@ -363,9 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // the pair's MMAs and arrivals are over
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -515,10 +572,10 @@ __global__ void __launch_bounds__(128)
       for (int i = 0; i < 4; ++i) {
         const int64_t m = m0 + 32 * i + lane;
         x[i] = 32 * i + lane < NT && m < p.M
-                   ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_words)
+                   ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_align)
                    : 0u;
       }
-      const uint32_t w = scale_word(wrow, kb, a.kb_n, a.w_words);
+      const uint32_t w = scale_word(wrow, kb, a.kb_n, a.w_align);
       const uint32_t slot = ch & 1u;
       if (!__all_sync(0xffffffffu,
                       !*abort_flag && mbar_wait(&sempty[slot], ((ch >> 1) & 1u) ^ 1u))) {
@@ -584,7 +641,7 @@ __global__ void __launch_bounds__(128)
       const int n = p.N - n0 - 4 * lane;   // columns of Y from this lane's first on
       if (OUT == CSA_BF16) {
         bf16* dst = static_cast<bf16*>(p.y) + at;
-        if (a.vec && n >= 4) {
+        if (a.y_align >= 16 && n >= 4) {
           *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]),
                                                       pack_bf16x2(v[2], v[3]));
         } else {
@@ -594,7 +651,7 @@ __global__ void __launch_bounds__(128)
         }
       } else {
         float* dst = static_cast<float*>(p.y) + at;
-        if (a.vec && n >= 4) {
+        if (a.y_align >= 16 && n >= 4) {
           store_vec(dst, v);
         } else {
 #pragma unroll
@@ -620,23 +677,44 @@ int sm_count() {
   return n;
 }
 
+// launch_pdl in clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, size_t smem,
+                            int cluster, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
 template <int OUT>
 cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   const Fp8GemmParams& p = a.p;
-  a.m_tiles = (int)((p.M + kTileM - 1) / kTileM);
+  a.m_tiles = (int)((p.M + 2 * kTileM - 1) / (2 * kTileM));
   a.n_tiles = (p.N + kN - 1) / kN;
   a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
   CUtensorMap mx, mw;
   if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, kTileM) ||
-      !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kN))
+      !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kN / 2))
     return cudaErrorInvalidValue;
   const int smem = kSmem + 1024;
   cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<OUT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t sms = sm_count();
-  const unsigned grid = (unsigned)(a.tiles < sms ? a.tiles : sms);
-  return launch_pdl(fp8_gemm_kernel<OUT>, dim3(grid), dim3(kThreads), smem, stream, mx, mw, a);
+  const int64_t pairs = sm_count() / 2;
+  return launch_clusters(fp8_gemm_kernel<OUT>, 2 * (a.tiles < pairs ? a.tiles : pairs), kThreads,
+                         smem, 2, stream, mx, mw, a);
 }
 
 template <int NT, int OUT>
@@ -660,21 +738,7 @@ cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
   auto kernel = fp8_gemm_few_kernel<NT, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.tiles * split));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)split;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, mx, mw, a, split);
+  return launch_clusters(kernel, a.tiles * split, 128, smem, split, stream, mx, mw, a, split);
 }
 
 template <int OUT>
@@ -697,11 +761,13 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream) {
   a.kb_n = (p.K + kBK - 1) / kBK;
   a.x_blocks = (p.x_cols + 127) / 128;
   a.w_rblocks = (p.N + 127) / 128;
-  a.x_words = a.x_blocks % kChunk == 0 && p.x_koff / 128 % kChunk == 0 &&
-              (reinterpret_cast<uintptr_t>(p.x_sf) & 3u) == 0;
-  a.w_words = a.kb_n % kChunk == 0 && (reinterpret_cast<uintptr_t>(p.w_sf) & 3u) == 0;
+  auto align = [](uintptr_t bits) { return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1; };
+  a.x_align = align(reinterpret_cast<uintptr_t>(p.x_sf) | (uintptr_t)a.x_blocks |
+                    (uintptr_t)(p.x_koff / 128));
+  a.w_align = align(reinterpret_cast<uintptr_t>(p.w_sf) | (uintptr_t)a.kb_n);
   const int64_t e = p.out == CSA_BF16 ? 2 : 4;
-  a.vec = (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0 && p.y_ld * e % 16 == 0;
+  const uintptr_t y = reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.y_ld * e);
+  a.y_align = y % 32 == 0 ? 32 : y % 16 == 0 ? 16 : 1;
   switch (p.out) {
     case CSA_BF16: return launch<CSA_BF16>(a, stream);
     case CSA_F32: return launch<CSA_F32>(a, stream);
