@@ -23,6 +23,15 @@ struct NormParams {
   void* codes;            // [T, d]
   void* scales;           // [T, ceil(d / 128)]
 };
+// SMs of the current device.
+inline int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 148;
+  return n;
+}
+
 cudaError_t launch_rmsnorm_fp8(int dtype, const NormParams& p, cudaStream_t stream);
 
 cudaError_t launch_fp8_quantize(int dtype, const void* x, int64_t ld, int64_t rows, int d,

@@ -16,19 +16,23 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
   return e > 0 ? (uint32_t)e : 0u;
 }
 
+// Infinities become NaN, so that the codes say so (the conversion would
+// saturate them) and the block's scale does not.
+template <int N>
+__device__ __forceinline__ void drop_infinities(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (isinf(v[i])) v[i] = __int_as_float(0x7fffffff);
+}
+
 // Codes of v 2^-e, rounded to nearest even (the product is exact: the factor is
-// a normal power of two).  NaN becomes the NaN code; an infinity, which the
-// conversion would saturate, becomes one here.
+// a normal power of two); v holds no infinity.  NaN becomes the NaN code.
 __device__ __forceinline__ uint32_t codes4(const float* v, uint32_t byte) {
   const float f = __uint_as_float((254u - byte) << 23);   // 2^(127 - byte), byte <= 247
-  float s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s[i] = v[i] * f;
-    if (isinf(s[i])) s[i] = __int_as_float(0x7fffffff);   // |v| <= 448 2^e where v is finite
-  }
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(s[0], s[1]), __NV_SATFINITE, __NV_E4M3) |
-         ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(s[2], s[3]), __NV_SATFINITE, __NV_E4M3)
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0] * f, v[1] * f), __NV_SATFINITE,
+                                            __NV_E4M3) |
+         ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] * f, v[3] * f), __NV_SATFINITE,
+                                             __NV_E4M3)
           << 16);
 }
 

@@ -75,14 +75,15 @@ struct GemmArgs {
 };
 
 // 2^e of the block and codes of 128 consecutive values of one row.
-__device__ __forceinline__ void store_codes128(const float* v, uint8_t* codes, uint8_t* scale) {
+__device__ __forceinline__ void store_codes128(float* v, uint8_t* codes, uint8_t* scale) {
   float a = 0.f;
 #pragma unroll
   for (int i = 0; i < 128; ++i) a = fmaxf(a, fabsf(v[i]));
-  if (isinf(a)) {
+  if (isinf(a)) {   // rare: the scale from the finite elements
+    drop_infinities<128>(v);
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 128; ++i) a = fmaxf(a, isinf(v[i]) ? 0.f : fabsf(v[i]));
+    for (int i = 0; i < 128; ++i) a = fmaxf(a, fabsf(v[i]));
   }
   const uint32_t byte = scale_byte(a);
   *scale = (uint8_t)byte;
@@ -399,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           if (i == 0) release();
           if (live && n0 + h * 128 < p.N)   // N is a multiple of 128
-            store_codes128(reinterpret_cast<const float*>(r),
+            store_codes128(reinterpret_cast<float*>(r),
                            static_cast<uint8_t*>(p.y) + at + h * 128,
                            p.y_sf + (at + h * 128) / 128);
         }
@@ -627,12 +628,11 @@ __global__ void __launch_bounds__(128)
     const int64_t at = (m0 + t) * p.y_ld + (int64_t)z * p.y_noff + n0 + 4 * lane;
     if constexpr (OUT == kFp8Out) {   // N is a multiple of 128
       float am = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-      am = warp_max(am);
+      am = warp_max(fmaxf(am, 0.f));   // fmaxf skips NaN
       if (isinf(am)) {   // warp-uniform
-        am = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) am = fmaxf(am, isinf(v[i]) ? 0.f : fabsf(v[i]));
-        am = warp_max(am);
+        drop_infinities<4>(v);
+        am = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+        am = warp_max(fmaxf(am, 0.f));
       }
       const uint32_t byte = scale_byte(am);
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + at) = codes4(v, byte);
@@ -667,14 +667,6 @@ __global__ void __launch_bounds__(128)
     tc_fence_after();
     tmem_dealloc(tmem, L::cols);
   }
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    n = 148;
-  return n;
 }
 
 // launch_pdl in clusters of `cluster` CTAs.
