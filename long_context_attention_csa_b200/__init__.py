@@ -469,6 +469,21 @@ def _fp8(t, shape, dev, what: str):
     return t.data_ptr()
 
 
+def _fp8_pair(x, shape, sshape, dev, codes, scales):
+    """Codes and scales to write, new where none are given, and their addresses."""
+    if codes is None:
+        codes = torch.empty_like(x, dtype=_E4M3, memory_format=torch.contiguous_format)
+        pc = codes.data_ptr()
+    else:
+        pc = _fp8(codes, shape, dev, "codes")
+    if scales is None:
+        scales = x.new_empty(sshape, dtype=_E8M0)
+        ps = scales.data_ptr()
+    else:
+        ps = _fp8(scales, sshape, dev, "scales")
+    return codes, scales, pc, ps
+
+
 def _row_stride(t, shape, dtype, dev, what: str):
     """Row stride of a [..., d] tensor: contiguous, or two-dimensional with
     contiguous rows."""
@@ -508,14 +523,13 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
     dt, shape = x.dtype, x.shape
     d = shape[-1]
     x_ld = _row_stride(x, shape, dt, dev, "x")
-    sshape = shape[:-1] + ((d + 127) // 128,)
     r_ld = s_ld = 0
     pr = ps = pg = None
     if residual is not None:
         r_ld = _row_stride(residual, shape, dt, dev, "residual")
         pr = residual.data_ptr()
         if sum_out is None:
-            sum_out = torch.empty(shape, dtype=dt, device=dev)
+            sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
             s_ld = d
         else:
             s_ld = _row_stride(sum_out, shape, dt, dev, "sum_out")
@@ -527,13 +541,10 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
                 or not gain.is_contiguous()):
             _refuse("gain: contiguous [d] float32")
         pg = gain.data_ptr()
-    if codes is None:
-        codes = torch.empty(shape, dtype=_E4M3, device=dev)
-    if scales is None:
-        scales = torch.empty(sshape, dtype=_E8M0, device=dev)
+    codes, scales, pc, psc = _fp8_pair(x, shape, shape[:-1] + ((d + 127) // 128,), dev, codes,
+                                       scales)
     _launch(dev, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, _dt(x), x.numel() // d, d,
-            x.data_ptr(), x_ld, pr, r_ld, pg, eps, ps, s_ld, _fp8(codes, shape, dev, "codes"),
-            _fp8(scales, sshape, dev, "scales"))
+            x.data_ptr(), x_ld, pr, r_ld, pg, eps, ps, s_ld, pc, psc)
     return (codes, scales) if sum_out is None else (codes, scales, sum_out)
 
 
@@ -546,17 +557,13 @@ def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
     ld = _row_stride(x, shape, x.dtype, dev, "x")
     if block_rows == 1:
         sshape = shape[:-1] + ((d + 127) // 128,)
-    elif x.dim() == 2:
+    elif len(shape) == 2:
         sshape = ((shape[0] + 127) // 128, (d + 127) // 128)
     else:
         _refuse("fp8_quantize: weights are [rows, d]")
-    if codes is None:
-        codes = torch.empty(shape, dtype=_E4M3, device=dev)
-    if scales is None:
-        scales = torch.empty(sshape, dtype=_E8M0, device=dev)
+    codes, scales, pc, ps = _fp8_pair(x, shape, sshape, dev, codes, scales)
     _launch(dev, stream, "fp8_quantize", lib().fp8_quantize, _dt(x), x.numel() // d, d,
-            x.data_ptr(), ld, block_rows, _fp8(codes, shape, dev, "codes"),
-            _fp8(scales, sshape, dev, "scales"))
+            x.data_ptr(), ld, block_rows, pc, ps)
     return codes, scales
 
 
@@ -564,26 +571,27 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
                stream=None):
     """y = x w^T of FP8 activations (codes [..., K], scales [..., ceil(K/128)])
     and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
-    bf16 or fp32.  ``y`` may be a two-dimensional column slice of a wider buffer."""
+    bf16 or fp32.  ``y``, whose dtype then counts, may be a two-dimensional
+    column slice of a wider buffer."""
     dev = _cuda_rows(x_codes, "fp8_matmul")
     shape = x_codes.shape
-    K, nb = shape[-1], (shape[-1] + 127) // 128
+    K = shape[-1]
+    nb = (K + 127) // 128
     if w_codes.dim() != 2:
         _refuse("w_codes: [N, K]")
     N = w_codes.shape[0]
-    yshape = shape[:-1] + (N,)
+    px = _fp8(x_codes, shape, dev, "x_codes")
+    pxs = _fp8(x_scales, shape[:-1] + (nb,), dev, "x_scales")
+    pw = _fp8(w_codes, (N, K), dev, "w_codes")
+    pws = _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales")
     if y is None:
-        y = torch.empty(yshape, dtype=out_dtype, device=dev)
+        y = x_codes.new_empty(shape[:-1] + (N,), dtype=out_dtype)
         y_ld = N
     else:
-        y_ld = _row_stride(y, yshape, y.dtype, dev, "y")
+        y_ld = _row_stride(y, shape[:-1] + (N,), y.dtype, dev, "y")
     ws = _ws(ws, 256, dev)
-    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), x_codes.numel() // K, N, K,
-            _fp8(x_codes, shape, dev, "x_codes"),
-            _fp8(x_scales, shape[:-1] + (nb,), dev, "x_scales"),
-            _fp8(w_codes, (N, K), dev, "w_codes"),
-            _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales"), y.data_ptr(), y_ld,
-            ws.data_ptr(), ws.numel())
+    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), x_codes.numel() // K, N, K, px,
+            pxs, pw, pws, y.data_ptr(), y_ld, ws.data_ptr(), ws.numel())
     return y
 
 

@@ -429,32 +429,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- few rows -------------------------------------------------------------------
 //
-// One CTA: 128 rows of W against up to NT rows of X over its share of K; the
-// cluster's CTAs hold the shares of one tile, leave float32 partials in shared
-// memory and add them in rank order (the sum's order does not depend on
-// timing), each for its share of the X rows.
+// One CTA: 128 rows of W against up to NT rows of X over its share of K.  A
+// cluster's CTAs hold the shares of one tile; each sends its float32 partials of
+// X row t to CTA t mod SPLIT, which adds them in rank order (the sum's order does
+// not depend on timing) and writes Y.  With one share, a bf16 or float32 tile
+// goes from TMEM to Y, a lane for each column.
 //   warp 0     TMA producer
 //   warp 1     TMEM owner, single-thread MMA issuer
 //   warp 2     scale tiles
-//   all four   TMEM -> shared memory -> sum over the cluster -> Y
-template <int NT>
+//   all four   the accumulator, lane = row of W = column of Y
+template <int NT, bool SUM>   // SUM: partials are gathered in shared memory
 struct Few {
   static constexpr int stage = kTileA + NT * kBK;
-  static constexpr int stages = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;
+  static constexpr int stages = NT <= 16 ? 5 : NT <= 32 ? 4 : NT <= 64 ? 3 : SUM ? 4 : 3;
   static constexpr int off_sf = stages * stage;
   static constexpr int off_bar = off_sf + 2 * 1024;
-  static constexpr int smem = off_bar + 256;
+  static constexpr int off_part = off_bar + 256;
+  static constexpr int smem = off_part + (SUM ? NT * kTileM * 4 : 0);
+  static constexpr int resident = smem + 2048 <= 233472 / 2 ? 2 : 1;   // CTAs per SM
   static constexpr uint32_t cols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
   static constexpr uint32_t sf_col = NT;   // after the accumulator: 2 x (4 + 4) columns
-  static_assert(NT * kTileM * 4 <= stages * stage, "partials reuse the ring");
-  static_assert(2 * (smem + 1024 + 1024) <= 233472, "two CTAs per SM");
+  static_assert(smem + 1024 <= 232448, "shared memory budget");
 };
 
-template <int NT, int OUT>
+template <int NT, int SPLIT, int OUT>
 __global__ void __launch_bounds__(128)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap map_x,
-                        const __grid_constant__ CUtensorMap map_w, GemmArgs a, int split) {
-  using L = Few<NT>;
+                        const __grid_constant__ CUtensorMap map_w, GemmArgs a) {
+  constexpr bool kSum = SPLIT > 1 || OUT == kFp8Out;
+  using L = Few<NT, kSum>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::off_bar);
@@ -466,16 +469,16 @@ __global__ void __launch_bounds__(128)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Fp8GemmParams& p = a.p;
-  const int rank = (int)(blockIdx.x % split);
-  const int64_t u = blockIdx.x / split;
+  const int rank = (int)(blockIdx.x % SPLIT);
+  const int64_t u = blockIdx.x / SPLIT;
   const int nt = (int)(u % a.n_tiles);
   const int64_t m0 = (u / a.n_tiles) % a.m_tiles * NT;
   const int z = (int)(u / a.n_tiles / a.m_tiles);
   const int n0 = nt * kTileM;
   // this CTA's chunks of K
   const int chunks = (a.kb_n + kChunk - 1) / kChunk;
-  const int c0 = (int)((int64_t)chunks * rank / split);
-  const int c1 = (int)((int64_t)chunks * (rank + 1) / split);
+  const int c0 = (int)((int64_t)chunks * rank / SPLIT);
+  const int c1 = (int)((int64_t)chunks * (rank + 1) / SPLIT);
   const int kb0 = c0 * kChunk, kb1 = min(c1 * kChunk, a.kb_n);
 
   if (threadIdx.x == 0) {
@@ -499,8 +502,12 @@ __global__ void __launch_bounds__(128)
   }
   tc_fence_before();
   __syncthreads();
+  if (SPLIT > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // W's share starts its way into L2 while the kernel before this one ends (a
+  // hint: should that kernel still write W, the loads below see what it wrote)
+  if (warp == 3 && kb0 + lane < kb1) tma_prefetch_3d(&map_w, (kb0 + lane) * kBK, n0, z);
   pdl_wait();
   pdl_trigger();
   auto give_up = [&](unsigned where) {
@@ -594,75 +601,98 @@ __global__ void __launch_bounds__(128)
   __syncwarp();
   // `done` follows every MMA, so every landed stage has been read
   if (!__all_sync(0xffffffffu, mbar_wait(done, 0))) give_up(0x814u);
-  __syncthreads();
+  if (SPLIT > 1) cluster_wait();
+  else __syncthreads();
   tc_fence_after();
-  float* part = reinterpret_cast<float*>(sm);   // [NT][128]
-  {
-    const uint32_t base = tmem_addr(tmem, (uint32_t)(warp * 32), 0);
-    constexpr int step = NT < 32 ? NT : 32;
-#pragma unroll 1
-    for (int t = 0; t < NT && m0 + t < p.M; t += step) {
-      uint32_t r[step];
-      if constexpr (step == 32) tmem_ld32(base + t, r);
-      else tmem_ld16(base + t, r);
-      tmem_ld_wait();
+  const uint32_t base = tmem_addr(tmem, (uint32_t)(warp * 32), 0);
+  constexpr int step = NT < 32 ? NT : 32;
+  const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
+  const int col = warp * 32 + lane;
+  const int64_t y0 = m0 * p.y_ld + (int64_t)z * p.y_noff + n0;
+  float* part = reinterpret_cast<float*>(sm + L::off_part);   // [row t / SPLIT][rank][128]
+  uint32_t to[SPLIT];
 #pragma unroll
-      for (int i = 0; i < step; ++i)
-        part[(t + i) * kTileM + warp * 32 + lane] = __uint_as_float(r[i]);
+  for (int j = 0; j < SPLIT; ++j)
+    to[j] = cluster_addr(part + rank * kTileM + col, (uint32_t)j);
+#pragma unroll 1
+  for (int t0 = 0; t0 < rows; t0 += step) {
+    uint32_t r[step];
+    if constexpr (step == 32) tmem_ld32(base + t0, r);
+    else tmem_ld16(base + t0, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < step; ++i) {
+      const int t = t0 + i;
+      const float v = __uint_as_float(r[i]);
+      if (t >= rows) continue;
+      if constexpr (kSum) {
+        // step is a multiple of SPLIT, so t mod SPLIT is i mod SPLIT
+        dsmem_st_f32(to[i % SPLIT] + (uint32_t)(t - i % SPLIT) * (kTileM * 4), v);
+      } else if (n0 + col < p.N) {
+        const int64_t at = y0 + t * p.y_ld + col;
+        if (OUT == CSA_BF16) static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
+        else static_cast<float*>(p.y)[at] = v;
+      }
     }
   }
   tc_fence_before();
-  if (split > 1) cluster_sync();
+  if (SPLIT > 1) cluster_sync();   // every partial has arrived
   else __syncthreads();
-  // a warp sums one X row's 128 columns, four a lane
-  const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
-  for (int t = rank + split * warp; t < rows; t += split * 4) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < split; ++j) {
-      const uint4 q = dsmem_ld_u32x4(part + t * kTileM + 4 * lane, (uint32_t)j);
-      v[0] += __uint_as_float(q.x);
-      v[1] += __uint_as_float(q.y);
-      v[2] += __uint_as_float(q.z);
-      v[3] += __uint_as_float(q.w);
-    }
-    const int64_t at = (m0 + t) * p.y_ld + (int64_t)z * p.y_noff + n0 + 4 * lane;
-    if constexpr (OUT == kFp8Out) {   // N is a multiple of 128
-      float am = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-      am = warp_max(fmaxf(am, 0.f));   // fmaxf skips NaN
-      if (isinf(am)) {   // warp-uniform
-        drop_infinities<4>(v);
-        am = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-        am = warp_max(fmaxf(am, 0.f));
-      }
-      const uint32_t byte = scale_byte(am);
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + at) = codes4(v, byte);
-      if (lane == 0) p.y_sf[at / 128] = (uint8_t)byte;
-    } else {
-      const int n = p.N - n0 - 4 * lane;   // columns of Y from this lane's first on
-      if (OUT == CSA_BF16) {
-        bf16* dst = static_cast<bf16*>(p.y) + at;
-        if (a.y_align >= 16 && n >= 4) {
-          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]),
-                                                      pack_bf16x2(v[2], v[3]));
+  if constexpr (kSum) {
+    // a warp adds one X row's partials, four columns a lane: side by side where
+    // Y's rows take 8- or 16-byte stores, else 32 apart
+    const bool vec = OUT == kFp8Out || a.y_align >= 16;
+    for (int k = warp; k * SPLIT + rank < rows; k += 4) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < SPLIT; ++j) {
+        const float* src = part + (k * SPLIT + j) * kTileM;
+        if (vec) {
+          const float4 q = *reinterpret_cast<const float4*>(src + 4 * lane);
+          v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
         } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n) dst[i] = __float2bfloat16_rn(v[i]);
+          for (int i = 0; i < 4; ++i) v[i] += src[lane + 32 * i];
         }
+      }
+      const int64_t row = y0 + (int64_t)(k * SPLIT + rank) * p.y_ld;
+      if constexpr (OUT == kFp8Out) {   // N, and rows of Y, are multiples of 128
+        float am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
+                                        fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));   // skips NaN
+        if (isinf(am)) {   // rare: the scale from the finite elements
+          drop_infinities<4>(v);
+          am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
+                                    fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));
+        }
+        const uint32_t byte = scale_byte(am);
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row + 4 * lane) =
+            codes4(v, byte);
+        if (lane == 0) p.y_sf[row / 128] = (uint8_t)byte;
       } else {
-        float* dst = static_cast<float*>(p.y) + at;
-        if (a.y_align >= 16 && n >= 4) {
-          store_vec(dst, v);
-        } else {
+        const int n = p.N - n0;   // columns of Y from this tile's first on
+        const bool whole = vec && 4 * lane + 4 <= n;
+        if (OUT == CSA_BF16) {
+          bf16* dst = static_cast<bf16*>(p.y) + row;
+          if (whole)
+            *reinterpret_cast<uint2*>(dst + 4 * lane) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n) dst[i] = v[i];
+          for (int i = 0; i < 4; ++i) {
+            const int c = vec ? 4 * lane + i : lane + 32 * i;
+            if (!whole && c < n) dst[c] = __float2bfloat16_rn(v[i]);
+          }
+        } else {
+          float* dst = static_cast<float*>(p.y) + row;
+          if (whole) store_vec(dst + 4 * lane, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = vec ? 4 * lane + i : lane + 32 * i;
+            if (!whole && c < n) dst[c] = v[i];
+          }
         }
       }
     }
   }
-  if (split > 1) cluster_sync();   // the others have read this CTA's partials
-  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::cols);
@@ -709,28 +739,38 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
                          smem, 2, stream, mx, mw, a);
 }
 
-template <int NT, int OUT>
-cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
-  using L = Few<NT>;
+template <int NT, int SPLIT, int OUT>
+cudaError_t launch_few(const GemmArgs& a, cudaStream_t stream) {
   const Fp8GemmParams& p = a.p;
-  a.m_tiles = (int)((p.M + NT - 1) / NT);
-  a.n_tiles = (p.N + kTileM - 1) / kTileM;
-  a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
-  // K shares: as many as keep two CTAs on every SM at once
-  const int chunks = (a.kb_n + kChunk - 1) / kChunk;
-  const int64_t room = 2 * sm_count();
-  int split = 1;
-  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room) split *= 2;
-  if (a.tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
   CUtensorMap mx, mw;
   if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, NT) ||
       !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kTileM))
     return cudaErrorInvalidValue;
-  const int smem = L::smem + 1024;
-  auto kernel = fp8_gemm_few_kernel<NT, OUT>;
+  const int smem = Few<NT, (SPLIT > 1 || OUT == kFp8Out)>::smem + 1024;
+  auto kernel = fp8_gemm_few_kernel<NT, SPLIT, OUT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kernel, a.tiles * split, 128, smem, split, stream, mx, mw, a, split);
+  return launch_clusters(kernel, a.tiles * SPLIT, 128, smem, SPLIT, stream, mx, mw, a);
+}
+
+template <int NT, int OUT>
+cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
+  const Fp8GemmParams& p = a.p;
+  a.m_tiles = (int)((p.M + NT - 1) / NT);
+  a.n_tiles = (p.N + kTileM - 1) / kTileM;
+  a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
+  // K shares: as many as fit the SMs at once
+  const int chunks = (a.kb_n + kChunk - 1) / kChunk;
+  const int64_t room = (int64_t)Few<NT, true>::resident * sm_count();
+  int split = 1;
+  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room) split *= 2;
+  if (a.tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
+  switch (split) {
+    case 1: return launch_few<NT, 1, OUT>(a, stream);
+    case 2: return launch_few<NT, 2, OUT>(a, stream);
+    case 4: return launch_few<NT, 4, OUT>(a, stream);
+    default: return launch_few<NT, 8, OUT>(a, stream);
+  }
 }
 
 template <int OUT>
@@ -738,9 +778,10 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   const Fp8GemmParams& p = a.p;
   const int64_t tiles = (int64_t)p.Z * ((p.M + kTileM - 1) / kTileM) * ((p.N + kN - 1) / kN);
   if (p.M > 128 && tiles >= 96) return launch_many<OUT>(a, stream);
+  const int64_t t128 = (int64_t)p.Z * ((p.M + 127) / 128) * ((p.N + 127) / 128);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
   if (p.M <= 32) return launch_few<32, OUT>(a, stream);
-  if (p.M <= 64) return launch_few<64, OUT>(a, stream);
+  if (p.M <= 64 || t128 * 4 < 3 * sm_count()) return launch_few<64, OUT>(a, stream);
   return launch_few<128, OUT>(a, stream);
 }
 
