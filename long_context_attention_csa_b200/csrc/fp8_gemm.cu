@@ -96,35 +96,34 @@ __device__ __forceinline__ void store_codes128(float* v, uint8_t* codes, uint8_t
   }
 }
 
-// Thirty-two consecutive values of one row, `n` of them inside Y.  `sectors`:
-// rows of Y start on 32-byte boundaries.
+// N consecutive words of a row that starts on a 32-byte or a 16-byte boundary.
+template <int N>
+__device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool sectors) {
+#pragma unroll
+  for (int q = 0; q < N / 8; ++q) {
+    if (sectors) {
+      store_sector(static_cast<uint32_t*>(dst) + 8 * q, w + 8 * q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        static_cast<uint4*>(dst)[2 * q + i] = make_uint4(
+            w[8 * q + 4 * i], w[8 * q + 4 * i + 1], w[8 * q + 4 * i + 2], w[8 * q + 4 * i + 3]);
+    }
+  }
+}
+
+// Thirty-two consecutive values of one row.
 template <int OUT>
-__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r, int n,
+__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r,
                                             bool sectors) {
   if constexpr (OUT == CSA_BF16) {
-    bf16* dst = static_cast<bf16*>(y) + at;
-    if (sectors && n >= 32) {
-      uint32_t w[16];
+    uint32_t w[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-      store_sector(dst, w);
-      store_sector(dst + 16, w + 8);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) dst[i] = __float2bfloat16_rn(__uint_as_float(r[i]));
-    }
+    for (int i = 0; i < 16; ++i)
+      w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    store_words<16>(static_cast<bf16*>(y) + at, w, sectors);
   } else {
-    float* dst = static_cast<float*>(y) + at;
-    if (sectors && n >= 32) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) store_sector(dst + 8 * q, r + 8 * q);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) dst[i] = __uint_as_float(r[i]);
-    }
+    store_words<32>(static_cast<float*>(y) + at, r, sectors);
   }
 }
 
@@ -151,8 +150,11 @@ constexpr int kOffSf = kStages * kStage;
 constexpr int kGroup = 4;                       // chunks whose scales are handed over together
 constexpr int kSfSlots = 3;                     // such groups in shared memory
 constexpr int kOffBar = kOffSf + kSfSlots * kGroup * kSfSlot;
-constexpr int kSmem = kOffBar + 256;
-constexpr int kThreads = 256;
+constexpr int kOffStage = kOffBar + 256;        // per epilogue warp: 32 rows x 16 columns, padded
+constexpr int kStagePitch = 17;
+constexpr int kEpiWarps = 4;   // eight: 2.5% slower, their stores come in bursts
+constexpr int kSmem = kOffStage + kEpiWarps * 32 * kStagePitch * 4;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kAcc1 = 232;               // second accumulator: columns 232 .. 487
 constexpr uint32_t kSfCol = 488;              // scales: 2 x (4 + 8) columns
 static_assert(kSmem + 1024 <= 232448, "shared memory budget");
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&cdone[0], 1);
     mbar_init(&cdone[1], 1);
     mbar_init(tfull, 1);
-    mbar_init(tfree, 8);
+    mbar_init(tfree, 2 * kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     const uint32_t free_bar = cluster_addr(tfree, 0);
+    float* stage = reinterpret_cast<float*>(sm + kOffStage) + quarter * 32 * kStagePitch;
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
@@ -393,16 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (OUT == kFp8Out) {
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          const int h = odd ? i : 1 - i;   // the half with the shared columns first
+          const int c0 = 128 * (odd ? i : 1 - i);   // the half with the shared columns first
           uint32_t r[128];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(base + h * 128 + q * 32, r + q * 32);
+          for (int q = 0; q < 4; ++q) tmem_ld32(base + c0 + q * 32, r + q * 32);
           tmem_ld_wait();
           if (i == 0) release();
-          if (live && n0 + h * 128 < p.N)   // N is a multiple of 128
-            store_codes128(reinterpret_cast<float*>(r),
-                           static_cast<uint8_t*>(p.y) + at + h * 128,
-                           p.y_sf + (at + h * 128) / 128);
+          if (live && n0 + c0 < p.N)   // N is a multiple of 128
+            store_codes128(reinterpret_cast<float*>(r), static_cast<uint8_t*>(p.y) + at + c0,
+                           p.y_sf + (at + c0) / 128);
         }
       } else {
 #pragma unroll 1
@@ -412,7 +414,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(base + cc, r);
           tmem_ld_wait();
           if (i == 0) release();
-          if (live && n0 + cc < p.N) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.y_align >= 32);
+          const int cols = p.N - n0 - cc;   // columns of Y from here on
+          if (cols >= 32 && a.y_align >= 16) {
+            if (live) store_row32<OUT>(p.y, at + cc, r, a.y_align >= 32);
+          } else if (cols > 0) {
+            // rows that start anywhere, or end here: through shared memory, so that
+            // a store's lanes lie side by side (a lane a row: 41 us for 1500 x 1300
+            // x 512)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              __syncwarp();
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                stage[lane * kStagePitch + c] = __uint_as_float(r[16 * half + c]);
+              __syncwarp();
+              const int c = 16 * half + (lane & 15);
+#pragma unroll 4
+              for (int q = lane >> 4; q < 32; q += 2) {
+                const int64_t m = m0 + quarter * 32 + q;
+                if (m < p.M && c < cols) {
+                  const int64_t to = m * p.y_ld + (int64_t)z * p.y_noff + n0 + cc + c;
+                  const float v = stage[q * kStagePitch + (lane & 15)];
+                  if (OUT == CSA_BF16) static_cast<bf16*>(p.y)[to] = __float2bfloat16_rn(v);
+                  else static_cast<float*>(p.y)[to] = v;
+                }
+              }
+            }
+          }
         }
       }
     }
@@ -505,9 +533,6 @@ __global__ void __launch_bounds__(128)
   if (SPLIT > 1) cluster_arrive();   // this CTA runs: its shared memory may be written
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // W's share starts its way into L2 while the kernel before this one ends (a
-  // hint: should that kernel still write W, the loads below see what it wrote)
-  if (warp == 3 && kb0 + lane < kb1) tma_prefetch_3d(&map_w, (kb0 + lane) * kBK, n0, z);
   pdl_wait();
   pdl_trigger();
   auto give_up = [&](unsigned where) {
@@ -759,11 +784,15 @@ cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
   a.m_tiles = (int)((p.M + NT - 1) / NT);
   a.n_tiles = (p.N + kTileM - 1) / kTileM;
   a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
-  // K shares: as many as fit the SMs at once
+  // K shares: as many as fit the SMs at once, of two chunks or more unless fewer
+  // than 48 CTAs would run (1 x 4096 x 4096: four shares 4.7 us, eight 5.2; 1 x
+  // 1024 x 4096: four 4.4, eight 3.7)
   const int chunks = (a.kb_n + kChunk - 1) / kChunk;
   const int64_t room = (int64_t)Few<NT, true>::resident * sm_count();
   int split = 1;
-  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room) split *= 2;
+  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room &&
+         (split * 4 <= chunks || a.tiles * split < 48))
+    split *= 2;
   if (a.tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
   switch (split) {
     case 1: return launch_few<NT, 1, OUT>(a, stream);
@@ -776,12 +805,26 @@ cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
 template <int OUT>
 cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   const Fp8GemmParams& p = a.p;
-  const int64_t tiles = (int64_t)p.Z * ((p.M + kTileM - 1) / kTileM) * ((p.N + kN - 1) / kN);
-  if (p.M > 128 && tiles >= 96) return launch_many<OUT>(a, stream);
-  const int64_t t128 = (int64_t)p.Z * ((p.M + 127) / 128) * ((p.N + 127) / 128);
+  const int64_t sms = sm_count();
+  auto tiles = [&](int64_t rows, int64_t cols) {
+    return (int64_t)p.Z * ((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols);
+  };
+  // The pairs' 256 x 256 tiles pay from about two thirds of a wave of K = 4096 or
+  // as much work in more waves (measured, us, pairs against 128 x 128 tiles: 768 x
+  // 4096 x 4096 18.1, 18.3; 512 x 4096 x 4096 16.7, 16.2; 4096 x 4096 x 1024 24.7,
+  // 28.5; 2048 x 2048 x 1024 10.6, 7.9).  Their epilogue is the slower one where
+  // rows of Y start anywhere, and shows once K is short (4097 x 4097 x 1024: 36.3,
+  // 30.1).
+  const int64_t pairs = tiles(2 * kTileM, kN);
+  if (pairs >= 32 && pairs * a.kb_n >= 1536 && (a.y_align >= 16 || a.kb_n >= 32))
+    return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
   if (p.M <= 32) return launch_few<32, OUT>(a, stream);
-  if (p.M <= 64 || t128 * 4 < 3 * sm_count()) return launch_few<64, OUT>(a, stream);
+  // 64-row tiles where the 128-row ones leave SMs idle that the others fill (512 x
+  // 4096 x 4096: 15.0 us against 16.2)
+  const int64_t t128 = tiles(128, kTileM);
+  if (p.M <= 64 || (5 * t128 > 3 * sms && t128 <= sms && tiles(64, kTileM) <= 2 * sms))
+    return launch_few<64, OUT>(a, stream);
   return launch_few<128, OUT>(a, stream);
 }
 

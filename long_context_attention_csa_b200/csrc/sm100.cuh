@@ -134,15 +134,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Brings one box into L2 only (a hint: nothing is written and nothing waits).
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int32_t c0, int32_t c1,
-                                                int32_t c2) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2)
-               : "memory");
-}
-
 // Untiled bulk copy of `bytes` contiguous bytes from global to shared memory
 // (both addresses 16-byte aligned, bytes a multiple of 16); completes `bar`'s
 // tx count.
