@@ -436,21 +436,22 @@ def grouped_output_projection(o, w_group, w_out, y=None, ws=None, stream=None):
 
 
 # The calls below may follow one another every few microseconds (one token's
-# norm and projections), so their checks build no message unless they fail.
+# norm and projections), so they ask each tensor for little and build no message
+# unless a check fails.
 
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
-_FP8_TYPES = (_E4M3, _E8M0, torch.uint8)
+_FP8_TYPES = frozenset((_E4M3, _E8M0, torch.uint8))
+_FLOATS = {torch.bfloat16: CSA_BF16, torch.float32: CSA_F32}
 
 
-def _launch(dev, stream, what, fn, *args):
-    """fn(*args, stream) on `dev`'s current stream unless one is given, with
-    `dev` current while it launches."""
-    raw = (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
-           else stream.cuda_stream)
-    if dev.index == torch.cuda.current_device():
+def _launch(idx, stream, what, fn, *args):
+    """fn(*args, stream) on device idx's current stream unless one is given,
+    with the device current while it launches."""
+    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+    if idx == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(idx):
             st = fn(*args, raw)
     if st != CSA_OK:
         raise CSAError(st, what)
@@ -460,36 +461,25 @@ def _refuse(what: str):
     raise CSAError(CSA_E_ARG, what)
 
 
-def _fp8(t, shape, dev, what: str):
-    """Address of contiguous FP8 codes or scales of the given shape on dev."""
-    if (t.dtype not in _FP8_TYPES or t.shape != shape or t.device != dev
+def _where(idx):
+    return "the CPU" if idx < 0 else f"cuda:{idx}"
+
+
+def _fp8(t, shape, idx, what: str):
+    """Address of contiguous FP8 codes or scales of the given shape on device idx."""
+    if (t.shape != shape or t.get_device() != idx or t.dtype not in _FP8_TYPES
             or not t.is_contiguous()):
-        _refuse(f"{what}: contiguous FP8 of shape {tuple(shape)} on {dev} expected, got "
-                f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        _refuse(f"{what}: contiguous FP8 of shape {tuple(shape)} on {_where(idx)} expected, got "
+                f"{t.dtype} {tuple(t.shape)} on {_where(t.get_device())}")
     return t.data_ptr()
 
 
-def _fp8_pair(x, shape, sshape, dev, codes, scales):
-    """Codes and scales to write, new where none are given, and their addresses."""
-    if codes is None:
-        codes = torch.empty_like(x, dtype=_E4M3, memory_format=torch.contiguous_format)
-        pc = codes.data_ptr()
-    else:
-        pc = _fp8(codes, shape, dev, "codes")
-    if scales is None:
-        scales = x.new_empty(sshape, dtype=_E8M0)
-        ps = scales.data_ptr()
-    else:
-        ps = _fp8(scales, sshape, dev, "scales")
-    return codes, scales, pc, ps
-
-
-def _row_stride(t, shape, dtype, dev, what: str):
+def _row_stride(t, shape, dtype, idx, what: str):
     """Row stride of a [..., d] tensor: contiguous, or two-dimensional with
     contiguous rows."""
-    if t.dtype != dtype or t.shape != shape or t.device != dev:
-        _refuse(f"{what}: {dtype} of shape {tuple(shape)} on {dev} expected, got {t.dtype} "
-                f"{tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.get_device() != idx or t.dtype != dtype:
+        _refuse(f"{what}: {dtype} of shape {tuple(shape)} on {_where(idx)} expected, got "
+                f"{t.dtype} {tuple(t.shape)} on {_where(t.get_device())}")
     if t.is_contiguous():
         return shape[-1]
     if len(shape) != 2 or t.stride(1) != 1 or t.stride(0) < shape[1]:
@@ -498,19 +488,36 @@ def _row_stride(t, shape, dtype, dev, what: str):
 
 
 def _cuda_rows(x, what: str):
-    """Device of a CUDA tensor [..., d] with d > 0."""
-    if not x.is_cuda or x.dim() < 1 or x.shape[-1] < 1:
+    """Device, shape and last dim (d > 0) of a CUDA tensor [..., d]."""
+    idx, shape = x.get_device(), x.shape
+    if idx < 0 or len(shape) < 1 or shape[-1] < 1:
         _refuse(f"{what}: a CUDA tensor [..., d]")
-    return x.device
+    return idx, shape, shape[-1]
 
 
-def _ws(ws, nbytes: int, dev):
-    """The workspace given, checked, or one of the call's own."""
+def _fp8_pair(x, shape, sshape, idx, codes, scales):
+    """Codes and scales to write, new where none are given, and their addresses."""
+    if codes is None:
+        codes = torch.empty_like(x, dtype=_E4M3, memory_format=torch.contiguous_format)
+        pc = codes.data_ptr()
+    else:
+        pc = _fp8(codes, shape, idx, "codes")
+    if scales is None:
+        scales = x.new_empty(sshape, dtype=_E8M0)
+        ps = scales.data_ptr()
+    else:
+        ps = _fp8(scales, sshape, idx, "scales")
+    return codes, scales, pc, ps
+
+
+def _ws(ws, nbytes: int, idx):
+    """Address and size of the workspace given, or of one of the call's own, and
+    the tensor that holds it."""
     if ws is None:
-        return workspace(nbytes, dev)
-    if ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous():
-        _refuse(f"ws: contiguous uint8 on {dev}")
-    return ws
+        ws = workspace(nbytes, torch.device("cuda", idx))
+    elif ws.get_device() != idx or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        _refuse(f"ws: contiguous uint8 on {_where(idx)}")
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, codes=None,
@@ -519,31 +526,30 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
     activations: codes [..., d] float8_e4m3fn and scales [..., ceil(d/128)]
     float8_e8m0fnu.  With a residual also returns x + residual (in ``sum_out``,
     which may be x or residual itself)."""
-    dev = _cuda_rows(x, "rmsnorm_fp8")
-    dt, shape = x.dtype, x.shape
-    d = shape[-1]
-    x_ld = _row_stride(x, shape, dt, dev, "x")
+    idx, shape, d = _cuda_rows(x, "rmsnorm_fp8")
+    dt = x.dtype
+    x_ld = _row_stride(x, shape, dt, idx, "x")
     r_ld = s_ld = 0
     pr = ps = pg = None
     if residual is not None:
-        r_ld = _row_stride(residual, shape, dt, dev, "residual")
+        r_ld = _row_stride(residual, shape, dt, idx, "residual")
         pr = residual.data_ptr()
         if sum_out is None:
             sum_out = torch.empty_like(x, memory_format=torch.contiguous_format)
             s_ld = d
         else:
-            s_ld = _row_stride(sum_out, shape, dt, dev, "sum_out")
+            s_ld = _row_stride(sum_out, shape, dt, idx, "sum_out")
         ps = sum_out.data_ptr()
     elif sum_out is not None:
         _refuse("sum_out needs a residual")
     if gain is not None:
-        if (gain.dtype != torch.float32 or gain.shape != (d,) or gain.device != dev
+        if (gain.shape != (d,) or gain.get_device() != idx or gain.dtype != torch.float32
                 or not gain.is_contiguous()):
-            _refuse("gain: contiguous [d] float32")
+            _refuse("gain: contiguous [d] float32 on x's device")
         pg = gain.data_ptr()
-    codes, scales, pc, psc = _fp8_pair(x, shape, shape[:-1] + ((d + 127) // 128,), dev, codes,
+    codes, scales, pc, psc = _fp8_pair(x, shape, shape[:-1] + ((d + 127) // 128,), idx, codes,
                                        scales)
-    _launch(dev, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, _dt(x), x.numel() // d, d,
+    _launch(idx, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, _FLOATS.get(dt, -1), x.numel() // d, d,
             x.data_ptr(), x_ld, pr, r_ld, pg, eps, ps, s_ld, pc, psc)
     return (codes, scales) if sum_out is None else (codes, scales, sum_out)
 
@@ -551,19 +557,18 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
 def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
     """FP8 activations of x [..., d] (block_rows 1), or FP8 weights of x
     [rows, d] (block_rows 128): codes and scales [ceil(rows/128), ceil(d/128)]."""
-    dev = _cuda_rows(x, "fp8_quantize")
-    shape = x.shape
-    d = shape[-1]
-    ld = _row_stride(x, shape, x.dtype, dev, "x")
+    idx, shape, d = _cuda_rows(x, "fp8_quantize")
+    dt = x.dtype
+    ld = _row_stride(x, shape, dt, idx, "x")
     if block_rows == 1:
         sshape = shape[:-1] + ((d + 127) // 128,)
     elif len(shape) == 2:
         sshape = ((shape[0] + 127) // 128, (d + 127) // 128)
     else:
         _refuse("fp8_quantize: weights are [rows, d]")
-    codes, scales, pc, ps = _fp8_pair(x, shape, sshape, dev, codes, scales)
-    _launch(dev, stream, "fp8_quantize", lib().fp8_quantize, _dt(x), x.numel() // d, d,
-            x.data_ptr(), ld, block_rows, pc, ps)
+    codes, scales, pc, ps = _fp8_pair(x, shape, sshape, idx, codes, scales)
+    _launch(idx, stream, "fp8_quantize", lib().fp8_quantize, _FLOATS.get(dt, -1), x.numel() // d,
+            d, x.data_ptr(), ld, block_rows, pc, ps)
     return codes, scales
 
 
@@ -573,25 +578,25 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
     and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
     bf16 or fp32.  ``y``, whose dtype then counts, may be a two-dimensional
     column slice of a wider buffer."""
-    dev = _cuda_rows(x_codes, "fp8_matmul")
-    shape = x_codes.shape
-    K = shape[-1]
-    nb = (K + 127) // 128
-    if w_codes.dim() != 2:
+    idx, shape, K = _cuda_rows(x_codes, "fp8_matmul")
+    lead, nb = shape[:-1], (K + 127) // 128
+    wshape = w_codes.shape
+    if len(wshape) != 2:
         _refuse("w_codes: [N, K]")
-    N = w_codes.shape[0]
-    px = _fp8(x_codes, shape, dev, "x_codes")
-    pxs = _fp8(x_scales, shape[:-1] + (nb,), dev, "x_scales")
-    pw = _fp8(w_codes, (N, K), dev, "w_codes")
-    pws = _fp8(w_scales, ((N + 127) // 128, nb), dev, "w_scales")
+    N = wshape[0]
+    px = _fp8(x_codes, shape, idx, "x_codes")
+    pxs = _fp8(x_scales, lead + (nb,), idx, "x_scales")
+    pw = _fp8(w_codes, (N, K), idx, "w_codes")
+    pws = _fp8(w_scales, ((N + 127) // 128, nb), idx, "w_scales")
     if y is None:
-        y = x_codes.new_empty(shape[:-1] + (N,), dtype=out_dtype)
+        y = x_codes.new_empty(lead + (N,), dtype=out_dtype)
         y_ld = N
     else:
-        y_ld = _row_stride(y, shape[:-1] + (N,), y.dtype, dev, "y")
-    ws = _ws(ws, 256, dev)
-    _launch(dev, stream, "fp8_matmul", lib().fp8_matmul, _dt(y), x_codes.numel() // K, N, K, px,
-            pxs, pw, pws, y.data_ptr(), y_ld, ws.data_ptr(), ws.numel())
+        out_dtype = y.dtype
+        y_ld = _row_stride(y, lead + (N,), out_dtype, idx, "y")
+    pws_, nws, ws = _ws(ws, 256, idx)
+    _launch(idx, stream, "fp8_matmul", lib().fp8_matmul, _FLOATS.get(out_dtype, -1),
+            x_codes.numel() // K, N, K, px, pxs, pw, pws, y.data_ptr(), y_ld, pws_, nws)
     return y
 
 
@@ -600,29 +605,29 @@ def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scale
     """Grouped output projection in FP8: o [T, H, c] (bf16 or fp32), w_group
     [g, d_g, (H/g) c] and w_out [d, g d_g] FP8 weights (the scales of w_group
     [g, d_g/128, (H/g) c/128]) -> y [T, d] bf16."""
-    dev = _cuda_rows(o, "grouped_output_projection_fp8")
-    if o.dim() != 3 or w_group.dim() != 3 or w_out.dim() != 2 or not o.is_contiguous():
+    idx, shape, c = _cuda_rows(o, "grouped_output_projection_fp8")
+    if len(shape) != 3 or w_group.dim() != 3 or w_out.dim() != 2 or not o.is_contiguous():
         _refuse("o: contiguous [T, H, c], w_group: [g, d_g, k], w_out: [d, g d_g]")
-    T, H, c = o.shape
+    T, H, c = shape
     g, dg, kg = w_group.shape
     d = w_out.shape[0]
-    if g * kg != H * c:
+    dt = _FLOATS.get(o.dtype, -1)
+    if g < 1 or g * kg != H * c:
         _refuse("w_group: [g, d_g, (H/g) c]")
     if H % g or kg % 128 or dg % 128:
         raise CSAError(CSA_E_UNSUPPORTED, "grouped_output_projection_fp8: g divides H, (H/g) c "
                        "and d_g are multiples of 128")
+    pg = _fp8(w_group, (g, dg, kg), idx, "w_group")
+    pgs = _fp8(w_group_scales, (g, dg // 128, kg // 128), idx, "w_group_scales")
+    po = _fp8(w_out, (d, g * dg), idx, "w_out")
+    pos = _fp8(w_out_scales, ((d + 127) // 128, g * dg // 128), idx, "w_out_scales")
     if y is None:
-        y = torch.empty((T, d), dtype=torch.bfloat16, device=dev)
-    elif _row_stride(y, (T, d), torch.bfloat16, dev, "y") != d:
+        y = o.new_empty((T, d), dtype=torch.bfloat16)
+    elif _row_stride(y, (T, d), torch.bfloat16, idx, "y") != d:
         _refuse("y: contiguous")
-    if ws is None:
-        ws = workspace(csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, _dt(o), 1, T, H, c, g * dg), dev)
-    else:
-        ws = _ws(ws, 0, dev)
-    _launch(dev, stream, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
-            _dt(o), T, H, c, g, dg, d, o.data_ptr(), _fp8(w_group, (g, dg, kg), dev, "w_group"),
-            _fp8(w_group_scales, (g, dg // 128, kg // 128), dev, "w_group_scales"),
-            _fp8(w_out, (d, g * dg), dev, "w_out"),
-            _fp8(w_out_scales, ((d + 127) // 128, g * dg // 128), dev, "w_out_scales"),
-            y.data_ptr(), ws.data_ptr(), ws.numel())
+    need = 0 if ws is not None else csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dt, 1, T, H, c,
+                                                        g * dg)
+    pws, nws, ws = _ws(ws, need, idx)
+    _launch(idx, stream, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
+            dt, T, H, c, g, dg, d, o.data_ptr(), pg, pgs, po, pos, y.data_ptr(), pws, nws)
     return y

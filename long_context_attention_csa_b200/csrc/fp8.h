@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace csa {
 
 constexpr int kFp8MaxNormDim = 32768;   // columns rmsnorm_fp8 holds in registers
@@ -23,12 +25,24 @@ struct NormParams {
   void* codes;            // [T, d]
   void* scales;           // [T, ceil(d / 128)]
 };
-// SMs of the current device.
+constexpr int kMaxDevices = 64;
+
+// The current device, or -1.
+inline int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev < kMaxDevices ? dev : -1;
+}
+
+// SMs of the current device (asked once per device).
 inline int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
+  static std::atomic<int> known[kMaxDevices];
+  const int dev = current_device();
+  int n = dev >= 0 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  if (dev < 0 ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    n = 148;
+    return 148;
+  known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -724,6 +724,17 @@ __global__ void __launch_bounds__(128)
   }
 }
 
+// Lets `kernel` take `smem` bytes on the current device; asked once per device.
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), int smem, std::atomic<bool>* done) {
+  const int dev = current_device();
+  if (dev >= 0 && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && dev >= 0) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 // launch_pdl in clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, size_t smem,
@@ -756,8 +767,8 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
       !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kN / 2))
     return cudaErrorInvalidValue;
   const int smem = kSmem + 1024;
-  cudaError_t e = cudaFuncSetAttribute(fp8_gemm_kernel<OUT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = allow_smem(fp8_gemm_kernel<OUT>, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t pairs = sm_count() / 2;
   return launch_clusters(fp8_gemm_kernel<OUT>, 2 * (a.tiles < pairs ? a.tiles : pairs), kThreads,
@@ -773,7 +784,8 @@ cudaError_t launch_few(const GemmArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   const int smem = Few<NT, (SPLIT > 1 || OUT == kFp8Out)>::smem + 1024;
   auto kernel = fp8_gemm_few_kernel<NT, SPLIT, OUT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   return launch_clusters(kernel, a.tiles * SPLIT, 128, smem, SPLIT, stream, mx, mw, a);
 }
