@@ -37,38 +37,57 @@ constexpr int kChunk = 4;         // scale blocks per TMEM word
 constexpr int kTileM = 128;       // MMA M
 constexpr int kTileA = kTileM * kBK;
 
-// Scale bytes b0 .. b0 + 3 of a row of `end` scales, block b's in byte b - b0.
-// Bytes at or past `end` are not read (0).  `align`: the row starts, and b0 and
-// `end` lie, on multiples of that many bytes.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int b0, int end, int align) {
-  if (b0 >= end) return 0;
-  if (align >= 4) return *reinterpret_cast<const uint32_t*>(row + b0);
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < kChunk; ++i)
-    if (b0 + i < end) w |= (uint32_t)row[b0 + i] << (8 * i);
-  return w;
-}
+// Rows of scale bytes [rows][blocks], read four bytes at a time.  `align`: rows
+// start, and the first blocks asked for lie, on multiples of that many bytes (16,
+// 4 or 1).
+struct ScaleRows {
+  const uint8_t *begin, *end;   // the whole tensor
+  int blocks, align;
 
-// Four consecutive scale words.
-__device__ __forceinline__ void scale_words(const uint8_t* row, int b0, int end, int align,
-                                            uint32_t* w) {
-  if (align >= 16) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (b0 < end) q = *reinterpret_cast<const uint4*>(row + b0);
-    w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
-  } else {
+  // Scales b0 .. b0 + 4 N - 1 of a row, block b0 + i's in byte i: in rows that
+  // start anywhere the aligned words around them, shifted.  Bytes of blocks past
+  // the row's last hold no scale of the row.
+  template <int N>
+  __device__ __forceinline__ void get(int64_t row, int b0, uint32_t* w) const {
+    const uint8_t* p = begin + row * blocks + b0;
+    if (N == 4 && align >= 16) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (b0 < blocks) q = *reinterpret_cast<const uint4*>(p);
+      w[0] = q.x; w[N > 1 ? 1 : 0] = q.y; w[N > 2 ? 2 : 0] = q.z; w[N > 3 ? 3 : 0] = q.w;
+      return;
+    }
+    if (align >= 4) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w[c] = scale_word(row, b0 + c * kChunk, end, align);
+      for (int c = 0; c < N; ++c)
+        w[c] = b0 + 4 * c < blocks ? reinterpret_cast<const uint32_t*>(p)[c] : 0u;
+      return;
+    }
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const uint8_t* lo = p - off;
+    if (lo >= begin && lo + 4 * (N + 1) <= end) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(lo);
+      uint32_t v[N + 1];
+#pragma unroll
+      for (int c = 0; c <= N; ++c) v[c] = q[c];
+#pragma unroll
+      for (int c = 0; c < N; ++c) w[c] = __funnelshift_r(v[c], v[c + 1], 8 * off);
+    } else {   // at the tensor's ends
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        w[c] = 0;
+#pragma unroll
+        for (int i = 4 * c; i < 4 * c + 4; ++i)
+          if (b0 + i < blocks) w[c] |= (uint32_t)p[i] << (8 * (i & 3));
+      }
+    }
   }
-}
+};
 
 struct GemmArgs {
   Fp8GemmParams p;
   int kb_n;              // scale blocks (stages) of K
-  int x_blocks;          // scale blocks of a row of X
+  ScaleRows xs, ws;      // scales of X and of all W
   int w_rblocks;         // scale block rows of one W
-  int x_align, w_align;  // 16, 4 or 1: what scale rows and the groups' first blocks lie on
   int y_align;           // 32, 16 or 1: the boundaries that rows of Y start on
   int64_t tiles;
   int m_tiles, n_tiles;
@@ -158,7 +177,7 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kAcc1 = 232;               // second accumulator: columns 232 .. 487
 constexpr uint32_t kSfCol = 488;              // scales: 2 x (4 + 8) columns
 static_assert(kSmem + 1024 <= 232448, "shared memory budget");
-static_assert(kGroup == 4, "scale_words loads four");
+static_assert(kGroup * kChunk == 16, "a group is what aligned rows load at once");
 
 template <int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -334,18 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t m0;
       tile_of(u, z, m0, n0);
       const int xb0 = z * (p.x_koff / 128);
-      const uint8_t* wrow = p.w_sf + ((int64_t)z * a.w_rblocks + n0 / 128) * a.kb_n;
-      const int wend1 = n0 / 128 + 1 < a.w_rblocks ? a.kb_n : 0;
+      const int64_t wr = (int64_t)z * a.w_rblocks + n0 / 128;
+      const bool second = n0 / 128 + 1 < a.w_rblocks;
       for (int kb = 0; kb < a.kb_n; kb += kGroup * kChunk, ++gr) {
         uint32_t x[4][kGroup], w[2][kGroup];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int64_t m = m0 + 32 * i + lane;
-          scale_words(p.x_sf + m * a.x_blocks, xb0 + kb, m < p.M ? a.x_blocks : 0, a.x_align,
-                      x[i]);
+          const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
+          a.xs.get<kGroup>(m < p.M ? m : p.M - 1, xb0 + kb, x[i]);
         }
-        scale_words(wrow, kb, a.kb_n, a.w_align, w[0]);
-        scale_words(wrow + a.kb_n, kb, wend1, a.w_align, w[1]);
+        a.ws.get<kGroup>(wr, kb, w[0]);
+        a.ws.get<kGroup>(second ? wr + 1 : wr, kb, w[1]);
         const uint32_t slot = gr % kSfSlots;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[slot],
                                                                ((gr / kSfSlots) & 1u) ^ 1u));
@@ -469,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int NT, bool SUM>   // SUM: partials are gathered in shared memory
 struct Few {
   static constexpr int stage = kTileA + NT * kBK;
-  static constexpr int stages = NT <= 16 ? 5 : NT <= 32 ? 4 : NT <= 64 ? 3 : SUM ? 4 : 3;
+  static constexpr int stages = NT <= 16 ? 5 : NT <= 32 ? 4 : NT <= 64 ? (SUM ? 3 : 4)
+                                : SUM ? 4 : 3;
   static constexpr int off_sf = stages * stage;
   static constexpr int off_bar = off_sf + 2 * 1024;
   static constexpr int off_part = off_bar + 256;
@@ -597,18 +616,20 @@ __global__ void __launch_bounds__(128)
     }
   } else if (warp == 2) {
     const int xb0 = z * (p.x_koff / 128);
-    const uint8_t* wrow = p.w_sf + ((int64_t)z * a.w_rblocks + nt) * a.kb_n;
+    const int64_t wr = (int64_t)z * a.w_rblocks + nt;
+    constexpr int kRows = NT < 32 ? 1 : NT / 32;   // of this lane
+    uint32_t x[4] = {0u, 0u, 0u, 0u}, w;
+    auto load = [&](int kb) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
+        a.xs.get<1>(m < p.M ? m : p.M - 1, xb0 + kb, &x[i]);
+      }
+      a.ws.get<1>(wr, kb, &w);
+    };
+    load(kb0);
     uint32_t ch = 0;
     for (int kb = kb0; kb < kb1; kb += kChunk, ++ch) {
-      uint32_t x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 32 * i + lane;
-        x[i] = 32 * i + lane < NT && m < p.M
-                   ? scale_word(p.x_sf + m * a.x_blocks, xb0 + kb, a.x_blocks, a.x_align)
-                   : 0u;
-      }
-      const uint32_t w = scale_word(wrow, kb, a.kb_n, a.w_align);
       const uint32_t slot = ch & 1u;
       if (!__all_sync(0xffffffffu,
                       !*abort_flag && mbar_wait(&sempty[slot], ((ch >> 1) & 1u) ^ 1u))) {
@@ -621,6 +642,7 @@ __global__ void __launch_bounds__(128)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sfull[slot]);
+      if (kb + kChunk < kb1) load(kb + kChunk);   // the fence would wait for it
     }
   }
   __syncwarp();
@@ -831,11 +853,17 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   if (pairs >= 32 && pairs * a.kb_n >= 1536 && (a.y_align >= 16 || a.kb_n >= 32))
     return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
-  if (p.M <= 32) return launch_few<32, OUT>(a, stream);
-  // 64-row tiles where the 128-row ones leave SMs idle that the others fill (512 x
-  // 4096 x 4096: 15.0 us against 16.2)
-  const int64_t t128 = tiles(128, kTileM);
-  if (p.M <= 64 || (5 * t128 > 3 * sms && t128 <= sms && tiles(64, kTileM) <= 2 * sms))
+  // Smaller row tiles share the epilogue among more SMs, at the price of reading W
+  // again: 32 rows where K <= 1024 and the tiles fit the SMs at once (100 x 256 x
+  // 640: 4.4 us, 128-row tiles 6.5), 64 rows where K <= 2048 and they do (777 x
+  // 1111 x 1040: 6.2, 7.9), where there are few at any K (300 x 300 x 8192: 5.9,
+  // 6.8), and where 128-row tiles leave SMs idle that these fill (512 x 4096 x
+  // 4096: 13.8, 16.2); else 128 rows (96 x 4096 x 4096: 7.0, 64-row tiles 8.0).
+  if (p.M <= 32 || (a.kb_n <= 8 && tiles(32, kTileM) <= sms))
+    return launch_few<32, OUT>(a, stream);
+  const int64_t t128 = tiles(128, kTileM), t64 = tiles(64, kTileM);
+  if (p.M <= 64 || t64 <= 32 || (a.kb_n <= 16 && t64 <= sms) ||
+      (5 * t128 > 3 * sms && t128 <= sms && t64 <= 2 * sms))
     return launch_few<64, OUT>(a, stream);
   return launch_few<128, OUT>(a, stream);
 }
@@ -847,12 +875,14 @@ cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream) {
   GemmArgs a{};
   a.p = p;
   a.kb_n = (p.K + kBK - 1) / kBK;
-  a.x_blocks = (p.x_cols + 127) / 128;
   a.w_rblocks = (p.N + 127) / 128;
   auto align = [](uintptr_t bits) { return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1; };
-  a.x_align = align(reinterpret_cast<uintptr_t>(p.x_sf) | (uintptr_t)a.x_blocks |
-                    (uintptr_t)(p.x_koff / 128));
-  a.w_align = align(reinterpret_cast<uintptr_t>(p.w_sf) | (uintptr_t)a.kb_n);
+  const int xb = (p.x_cols + 127) / 128;
+  a.xs = {p.x_sf, p.x_sf + p.M * xb, xb,
+          align(reinterpret_cast<uintptr_t>(p.x_sf) | (uintptr_t)xb |
+                (uintptr_t)(p.x_koff / 128))};
+  a.ws = {p.w_sf, p.w_sf + (int64_t)p.Z * a.w_rblocks * a.kb_n, a.kb_n,
+          align(reinterpret_cast<uintptr_t>(p.w_sf) | (uintptr_t)a.kb_n)};
   const int64_t e = p.out == CSA_BF16 ? 2 : 4;
   const uintptr_t y = reinterpret_cast<uintptr_t>(p.y) | (uintptr_t)(p.y_ld * e);
   a.y_align = y % 32 == 0 ? 32 : y % 16 == 0 ? 16 : 1;
