@@ -430,7 +430,8 @@ csa_status grouped_output_projection(int32_t dtype, int64_t T, int32_t H, int32_
  *   may be x or residual itself (same pointer and stride).  Row strides in
  *   bytes are multiples of 16 and pointers 16-byte aligned.  The norm is taken
  *   of the unrounded h.  A row whose sum of squares is beyond float32 is
- *   scaled down first; a row with an infinity gives NaN there and 0 elsewhere.
+ *   scaled down first; a row with an infinity gives NaN there and 0 elsewhere,
+ *   and an element whose h gain is beyond float32 gives NaN.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad dtype, T < 0, d < 1, a
  * stride below d, eps < 0 or NaN, sum_out without residual); CSA_E_UNSUPPORTED
  * (d not a multiple of 16, or above 32768).
@@ -458,7 +459,7 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  * its last bits between values of M, which choose the split of K.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad out_dtype, negative M or
  * N, K < 1, y_ld < N), CSA_E_UNSUPPORTED (K not a multiple of 16, or M, N, K
- * beyond 2^31 - 1), CSA_E_WORKSPACE.
+ * beyond 2^30), CSA_E_WORKSPACE.
  */
 csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const void* x_codes,
                       const void* x_scales, const void* w_codes, const void* w_scales, void* y,
@@ -472,7 +473,8 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
  * w_group: [g, d_g, (H/g) c] codes, w_group_scales [g, d_g/128, (H/g) c/128];
  * w_out: [d, g d_g] codes, w_out_scales [ceil(d/128), g d_g/128]; y (out):
  * [T, d] bf16.  ws: >= csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dtype, 1, T,
- * H, c, g d_g, 0, 0).
+ * H, c, g d_g, 0, 0); it holds the codes of o and v during the call, so calls
+ * that overlap on the GPU need one each.
  * Errors: CSA_E_ARG, CSA_E_WORKSPACE, and CSA_E_UNSUPPORTED unless H % g == 0
  * and (H/g) c and d_g are multiples of 128.
  */

@@ -412,8 +412,7 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
                       int64_t y_ld, void* ws, size_t ws_bytes, void* stream) {
   if (out_dtype != CSA_F32 && out_dtype != CSA_BF16) return CSA_E_ARG;
   if (M < 0 || N < 0 || K < 1 || y_ld < N) return CSA_E_ARG;
-  if (K % 16 != 0 || M > 0x7fffffffLL || N > 0x7fffffffLL || K > 0x7fffffffLL)
-    return CSA_E_UNSUPPORTED;
+  if (K % 16 != 0 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim) return CSA_E_UNSUPPORTED;
   if (M == 0 || N == 0) return CSA_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return CSA_E_ARG;
   if (!aligned16(x_codes) || !aligned16(w_codes) ||
@@ -439,7 +438,8 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
 }
 
 // Workspace of grouped_output_projection_fp8: past the status word the codes
-// and scales of o and v, each on a 256-byte boundary.
+// and scales of o and v, each on a 256-byte boundary whatever ws starts on (the
+// kernels store whole sectors there).
 static size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, int32_t c,
@@ -451,7 +451,7 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   if (T < 0 || H <= 0 || c <= 0 || g <= 0 || d_g <= 0 || d <= 0) return CSA_E_ARG;
   const int64_t hc = (int64_t)H * c, gd = (int64_t)g * d_g;
   if (H % g != 0 || (hc / g) % 128 != 0 || d_g % 128 != 0) return CSA_E_UNSUPPORTED;
-  if (T > 0x7fffffffLL || hc > 0x7fffffffLL || gd > 0x7fffffffLL || g > 65535)
+  if (T > kFp8MaxDim || hc > kFp8MaxDim || gd > kFp8MaxDim || d > kFp8MaxDim || g > 65535)
     return CSA_E_UNSUPPORTED;
   if (T == 0) return CSA_OK;
   if (!o || !w_group || !w_group_scales || !w_out || !w_out_scales || !y) return CSA_E_ARG;
@@ -460,7 +460,8 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   if (!ws || !aligned16(ws) ||
       ws_bytes < csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dtype, 1, T, H, c, gd, 0, 0))
     return CSA_E_WORKSPACE;
-  uint8_t* oc = static_cast<uint8_t*>(ws) + kWsScratch;
+  uint8_t* oc = reinterpret_cast<uint8_t*>(
+      up256(reinterpret_cast<uintptr_t>(static_cast<uint8_t*>(ws) + kWsScratch)));
   uint8_t* os = oc + up256((size_t)T * hc);
   uint8_t* vc = os + up256((size_t)T * (hc / 128));
   uint8_t* vs = vc + up256((size_t)T * gd);
@@ -518,7 +519,7 @@ size_t csa_workspace_bytes(int32_t op, int32_t dtype, int64_t B, int64_t Tq, int
     case CSA_OP_OUT_PROJ_FP8: {
       if (H < 0 || c < 0) return 0;
       const size_t T = (size_t)B * (size_t)Tq, hc = (size_t)H * (size_t)c;
-      return kWsScratch + up256(T * hc) + up256(T * (hc / 128)) + up256(T * (size_t)N) +
+      return kWsScratch + 256 + up256(T * hc) + up256(T * (hc / 128)) + up256(T * (size_t)N) +
              up256(T * ((size_t)N / 128));
     }
     case CSA_OP_INDEXER:

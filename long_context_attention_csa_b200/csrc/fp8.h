@@ -11,6 +11,8 @@ namespace csa {
 
 constexpr int kFp8MaxNormDim = 32768;   // columns rmsnorm_fp8 holds in registers
 
+constexpr int64_t kFp8MaxDim = 1 << 30;  // rows and columns of a product: tile ends fit 32 bits
+
 struct NormParams {
   int64_t T;
   int d;

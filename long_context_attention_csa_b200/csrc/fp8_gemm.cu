@@ -131,18 +131,33 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool s
   }
 }
 
-// Thirty-two consecutive values of one row.
+// Thirty-two consecutive values of one row that starts on a 16-byte boundary (32
+// with `sectors`), `n` of them inside Y.
 template <int OUT>
-__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r,
+__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r, int n,
                                             bool sectors) {
   if constexpr (OUT == CSA_BF16) {
-    uint32_t w[16];
+    bf16* dst = static_cast<bf16*>(y) + at;
+    if (n >= 32) {
+      uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-    store_words<16>(static_cast<bf16*>(y) + at, w, sectors);
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+      store_words<16>(dst, w, sectors);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) dst[i] = __float2bfloat16_rn(__uint_as_float(r[i]));
+    }
   } else {
-    store_words<32>(static_cast<float*>(y) + at, r, sectors);
+    float* dst = static_cast<float*>(y) + at;
+    if (n >= 32) {
+      store_words<32>(dst, r, sectors);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) dst[i] = __uint_as_float(r[i]);
+    }
   }
 }
 
@@ -169,15 +184,56 @@ constexpr int kOffSf = kStages * kStage;
 constexpr int kGroup = 4;                       // chunks whose scales are handed over together
 constexpr int kSfSlots = 3;                     // such groups in shared memory
 constexpr int kOffBar = kOffSf + kSfSlots * kGroup * kSfSlot;
-constexpr int kOffStage = kOffBar + 256;        // per epilogue warp: 32 rows x 16 columns, padded
-constexpr int kStagePitch = 17;
 constexpr int kEpiWarps = 4;   // eight: 2.5% slower, their stores come in bursts
+constexpr int kOffStage = kOffBar + 256;        // per epilogue warp: 32 rows of 16 words, padded
+constexpr int kStagePitch = 17;
 constexpr int kSmem = kOffStage + kEpiWarps * 32 * kStagePitch * 4;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kAcc1 = 232;               // second accumulator: columns 232 .. 487
 constexpr uint32_t kSfCol = 488;              // scales: 2 x (4 + 8) columns
 static_assert(kSmem + 1024 <= 232448, "shared memory budget");
 static_assert(kGroup * kChunk == 16, "a group is what aligned rows load at once");
+
+// Thirty-two columns of a warp's `rows` rows (lane = row), `n` of them inside Y,
+// whose rows start anywhere: through shared memory, so that a store's lanes lie
+// side by side.
+template <int OUT>
+__device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, const uint32_t* r,
+                                             int rows, int n, uint32_t* stage,
+                                             int lane) {
+  const int half = lane >> 4, c = lane & 15;
+  if constexpr (OUT == CSA_BF16) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      stage[lane * kStagePitch + i] =
+          pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    __syncwarp();
+    // a row a store, a column a lane (two rows of pairs, where rows start on 4-byte
+    // boundaries: 4097 x 4098 x 1024 35.6 us, this way 28.7)
+    bf16* dst = static_cast<bf16*>(y) + at + lane;
+#pragma unroll 8
+    for (int q = 0; q < 32; ++q, dst += ld) {
+      const uint32_t w = stage[q * kStagePitch + (lane >> 1)];
+      if (q < rows && lane < n)
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)((lane & 1) ? w >> 16 : w);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = r[16 * h + i];
+      __syncwarp();
+      uint32_t* dst = static_cast<uint32_t*>(y) + at + half * ld + 16 * h + c;
+#pragma unroll 8
+      for (int q = half; q < 32; q += 2, dst += 2 * ld) {
+        const uint32_t w = stage[q * kStagePitch + c];
+        if (q < rows && 16 * h + c < n) *dst = w;
+      }
+    }
+  }
+}
 
 template <int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -281,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t it = 0, ch = 0, gr = 0, n = 0;   // stages, chunks, groups, tiles
       bool landed = false;                      // stage `it` is known to have landed
       for (int64_t u = first; u < a.tiles; u += step, ++n) {
-        if (*abort_flag || (n > 0 && !mbar_wait_cluster(tfree, (n - 1) & 1u))) {
+        if (*abort_flag || (n > 0 && !mbar_wait(tfree, (n - 1) & 1u))) {
           give_up(0x802u);
           break;
         }
@@ -389,11 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3;
     const uint32_t free_bar = cluster_addr(tfree, 0);
-    float* stage = reinterpret_cast<float*>(sm + kOffStage) + quarter * 32 * kStagePitch;
+    uint32_t* stage =
+        reinterpret_cast<uint32_t*>(sm + kOffStage) + quarter * 32 * kStagePitch;
     auto release = [&]() {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(free_bar);
+      if (lane == 0) mbar_arrive_cluster_exec(free_bar);
     };
     uint32_t n = 0;
     for (int64_t u = first; u < a.tiles; u += step, ++n) {
@@ -432,32 +489,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(base + cc, r);
           tmem_ld_wait();
           if (i == 0) release();
-          const int cols = p.N - n0 - cc;   // columns of Y from here on
-          if (cols >= 32 && a.y_align >= 16) {
-            if (live) store_row32<OUT>(p.y, at + cc, r, a.y_align >= 32);
-          } else if (cols > 0) {
-            // rows that start anywhere, or end here: through shared memory, so that
-            // a store's lanes lie side by side (a lane a row: 41 us for 1500 x 1300
-            // x 512)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              __syncwarp();
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                stage[lane * kStagePitch + c] = __uint_as_float(r[16 * half + c]);
-              __syncwarp();
-              const int c = 16 * half + (lane & 15);
-#pragma unroll 4
-              for (int q = lane >> 4; q < 32; q += 2) {
-                const int64_t m = m0 + quarter * 32 + q;
-                if (m < p.M && c < cols) {
-                  const int64_t to = m * p.y_ld + (int64_t)z * p.y_noff + n0 + cc + c;
-                  const float v = stage[q * kStagePitch + (lane & 15)];
-                  if (OUT == CSA_BF16) static_cast<bf16*>(p.y)[to] = __float2bfloat16_rn(v);
-                  else static_cast<float*>(p.y)[to] = v;
-                }
-              }
-            }
+          if (n0 + cc >= p.N) continue;
+          if (a.y_align >= 16) {
+            if (live) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.y_align >= 32);
+          } else {
+            const int64_t m = m0 + quarter * 32;   // this warp's first row
+            store_tile32<OUT>(p.y, m * p.y_ld + (int64_t)z * p.y_noff + n0 + cc, p.y_ld, r,
+                              (int)(p.M - m < 32 ? p.M - m : 32), p.N - n0 - cc, stage,
+                              lane);
           }
         }
       }
@@ -843,14 +882,12 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   auto tiles = [&](int64_t rows, int64_t cols) {
     return (int64_t)p.Z * ((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols);
   };
-  // The pairs' 256 x 256 tiles pay from about two thirds of a wave of K = 4096 or
-  // as much work in more waves (measured, us, pairs against 128 x 128 tiles: 768 x
-  // 4096 x 4096 18.1, 18.3; 512 x 4096 x 4096 16.7, 16.2; 4096 x 4096 x 1024 24.7,
-  // 28.5; 2048 x 2048 x 1024 10.6, 7.9).  Their epilogue is the slower one where
-  // rows of Y start anywhere, and shows once K is short (4097 x 4097 x 1024: 36.3,
-  // 30.1).
+  // The pairs' 256 x 256 tiles pay from about two thirds of a wave of K = 4096, or as
+  // much work in more waves (measured, us, pairs against 128 x 128 tiles: 768 x 4096
+  // x 4096 17.3, 17.7; 512 x 4096 x 4096 16.2, 14.4; 4096 x 2048 x 1024 13.4, 15.2;
+  // 2048 x 2048 x 2048 12.5, 11.3).
   const int64_t pairs = tiles(2 * kTileM, kN);
-  if (pairs >= 32 && pairs * a.kb_n >= 1536 && (a.y_align >= 16 || a.kb_n >= 32))
+  if (pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536))
     return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
   // Smaller row tiles share the epilogue among more SMs, at the price of reading W

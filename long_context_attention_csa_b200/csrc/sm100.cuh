@@ -255,6 +255,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
                : "memory");
 }
 
+// The same without the cluster-wide ordering of this thread's memory accesses
+// (a fence that takes about a microsecond): for what TMEM and tcgen05 fences order.
+__device__ __forceinline__ void mbar_arrive_cluster_exec(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // mbar_wait that also orders what other CTAs of the cluster did before they
 // arrived.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,

@@ -92,6 +92,28 @@ def test_quantize_row_stride_and_shapes():
     assert c3.shape == (0, 512) and s3.shape == (0, 4)
 
 
+def bits(t):
+    return t.view(torch.uint8) if t.element_size() == 1 else t
+
+
+@pytest.mark.parametrize("dtype,shift", [(torch.bfloat16, 8), (torch.float32, 4)])
+def test_rows_on_16_byte_boundaries(dtype, shift):
+    """Rows that start 16 bytes off a 32-byte boundary, in every operand."""
+    def off(t):   # the same values, 16 bytes into a wider buffer
+        wide = torch.zeros(t.shape[0], t.shape[1] + 2 * shift, dtype=t.dtype, device=DEV)
+        wide[:, shift:-shift] = t
+        return wide[:, shift:-shift]
+
+    x, r = normal((150, 528), dtype, 1), normal((150, 528), dtype, 2)
+    xo, ro = off(x), off(r)
+    assert xo.data_ptr() % 32 == 16
+    for br in (1, 128):
+        for a, b in zip(csa.fp8_quantize(xo, br), csa.fp8_quantize(x, br)):
+            assert torch.equal(bits(a), bits(b))
+    for a, b in zip(csa.rmsnorm_fp8(xo, ro, sum_out=ro), csa.rmsnorm_fp8(x, r)):
+        assert torch.equal(bits(a), bits(b))
+
+
 def test_quantize_past_2_31_elements():
     """Offsets beyond 32 bits, in the input and in the codes."""
     rows, d = 66000, 32768
@@ -170,8 +192,7 @@ def test_rmsnorm_in_place_and_strided():
     into = wide[:, 512:]
     got = csa.rmsnorm_fp8(x, into, sum_out=into)       # the residual stream updated in place
     for a, b in zip(got, want):
-        assert torch.equal(a.view(torch.uint8) if a.element_size() == 1 else a,
-                           b.view(torch.uint8) if b.element_size() == 1 else b)
+        assert torch.equal(bits(a), bits(b))
     assert (wide[:, :512] == 0).all()
     x2 = x.clone()
     csa.rmsnorm_fp8(x2, r, sum_out=x2)
@@ -225,7 +246,8 @@ def check_matmul(y, xc, xs, wc, ws, what=""):
     (1, 1, 16), (1, 128, 128), (1, 8192, 4096), (2, 131, 144), (16, 256, 512), (17, 129, 528),
     (32, 1000, 4096), (33, 257, 640), (64, 520, 1024), (65, 512, 2064), (100, 300, 16384),
     (128, 256, 512), (129, 257, 1040), (200, 1111, 272), (257, 4096, 768), (513, 999, 1552),
-    (1000, 1024, 4096), (2049, 2300, 1024),
+    (1000, 1024, 4096), (2049, 2300, 1024), (2049, 4090, 2048), (1100, 4097, 2064),
+    (700, 16384, 528), (4096, 4104, 1040),
 ])
 def test_matmul(M, N, K, out):
     xc, xs, wc, ws = operands(M, N, K, M + N + K)
@@ -240,6 +262,27 @@ def test_matmul_of_integers_is_exact(M, N, K):
     xc, xs, wc, ws = operands(M, N, K, 7, integers=True)
     y = csa.fp8_matmul(xc, xs, wc, ws, out_dtype=torch.float32)
     assert torch.equal(y.double(), values(xc, xs, 1) @ values(wc, ws, 128).t())
+
+
+def test_matmul_of_slices_of_a_batch():
+    """Rows from the middle of a batch: scales that start anywhere."""
+    xc, xs, wc, ws = operands(900, 300, 1168, 9)
+    for a, b in ((1, 2), (3, 40), (7, 300), (899, 900), (0, 900)):
+        y = csa.fp8_matmul(xc[a:b], xs[a:b], wc, ws)
+        check_matmul(y, xc[a:b], xs[a:b], wc, ws)
+
+
+def test_matmul_into_an_aligned_slice_by_pairs():
+    """The many-row kernel into column slices that start 16 and 32 bytes apart."""
+    xc, xs, wc, ws = operands(2048, 2048, 2048, 5)
+    want = csa.fp8_matmul(xc, xs, wc, ws)
+    check_matmul(want, xc, xs, wc, ws)
+    for at in (0, 8, 16):
+        wide = torch.full((2050, 2048 + 48), 9.0, dtype=torch.bfloat16, device=DEV)
+        csa.fp8_matmul(xc, xs, wc, ws, y=wide[:2048, at:at + 2048])
+        assert torch.equal(wide[:2048, at:at + 2048], want)
+        assert (wide[:2048, :at] == 9).all() and (wide[:2048, at + 2048:] == 9).all()
+        assert (wide[2048:] == 9).all()
 
 
 def test_matmul_into_a_slice_leaves_the_rest():
@@ -353,6 +396,17 @@ def test_projection(T, H, c, g, dg, d):
 def test_projection_of_float32_rows():
     x = proj_inputs(70, 8, 64, 2, 128, 200, 1, torch.float32)
     check_proj(csa.grouped_output_projection_fp8(*x), *x)
+
+
+def test_projection_with_a_workspace_on_a_16_byte_boundary():
+    for T in (20, 3000):
+        x = proj_inputs(T, 8, 256, 4, 256, 640, T)
+        n = csa.csa_workspace_bytes(csa.CSA_OP_OUT_PROJ_FP8, torch.bfloat16, 1, T, 8, 256, 1024)
+        ws = csa.workspace(n + 16)[16:]
+        assert ws.data_ptr() % 32 == 16
+        assert torch.equal(csa.grouped_output_projection_fp8(*x, ws=ws),
+                           csa.grouped_output_projection_fp8(*x))
+        assert csa.csa_check_status(ws) == (csa.CSA_OK, 0)
 
 
 def test_projection_8k_sampled():
