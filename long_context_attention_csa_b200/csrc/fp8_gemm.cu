@@ -532,17 +532,23 @@ struct Few {
   static constexpr int off_bar = off_sf + 2 * 1024;
   static constexpr int off_part = off_bar + 256;
   static constexpr int smem = off_part + (SUM ? NT * kTileM * 4 : 0);
-  static constexpr int resident = smem + 2048 <= 233472 / 2 ? 2 : 1;   // CTAs per SM
   static constexpr uint32_t cols = NT <= 16 ? 32 : NT <= 32 ? 64 : NT <= 64 ? 128 : 256;
   static constexpr uint32_t sf_col = NT;   // after the accumulator: 2 x (4 + 4) columns
   static_assert(smem + 1024 <= 232448, "shared memory budget");
 };
 
+// Codes need the largest of 128 columns of a row, so where one CTA has the whole
+// sum and 128 rows, X takes the MMA's M and a lane holds its row's columns (128
+// rows gathered in shared memory and reduced a warp a row: 12 us a CTA).
+template <int NT, int SPLIT, int OUT>
+constexpr bool few_rows_on_m = NT == 128 && SPLIT == 1 && OUT == kFp8Out;
+
 template <int NT, int SPLIT, int OUT>
 __global__ void __launch_bounds__(128)
     fp8_gemm_few_kernel(const __grid_constant__ CUtensorMap map_x,
                         const __grid_constant__ CUtensorMap map_w, GemmArgs a) {
-  constexpr bool kSum = SPLIT > 1 || OUT == kFp8Out;
+  constexpr bool kRows = few_rows_on_m<NT, SPLIT, OUT>;
+  constexpr bool kSum = (SPLIT > 1 || OUT == kFp8Out) && !kRows;
   using L = Few<NT, kSum>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -628,8 +634,8 @@ __global__ void __launch_bounds__(128)
           if (ok) {
             tc_fence_after();
             const uint32_t ss = smem_u32(sm + L::off_sf + slot * 1024);
-            tmem_cp_32x128b_x4(sfa, smem_desc(ss, 16, 128, 0));
-            tmem_cp_32x128b_x4(sfb, smem_desc(ss + 512, 16, 128, 0));
+            tmem_cp_32x128b_x4(kRows ? sfb : sfa, smem_desc(ss, 16, 128, 0));
+            tmem_cp_32x128b_x4(kRows ? sfa : sfb, smem_desc(ss + 512, 16, 128, 0));
           }
         }
         if (!ok || !mbar_wait(&full[s], (it / L::stages) & 1u)) {
@@ -642,8 +648,9 @@ __global__ void __launch_bounds__(128)
         const uint32_t idesc = idesc_mxf8_e4m3(kTileM, NT, id, id);
 #pragma unroll
         for (int kk = 0; kk < kBK / 32; ++kk)
-          mma_mxf8_ss(tmem, smem_desc(sa + kk * 32, 16, 1024, 2),
-                      smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc, sfa | (id << 30),
+          mma_mxf8_ss(tmem, smem_desc(sa + (kRows ? kTileA : 0) + kk * 32, 16, 1024, 2),
+                      smem_desc(sa + (kRows ? 0 : kTileA) + kk * 32, 16, 1024, 2), idesc,
+                      sfa | (id << 30),
                       sfb | (id << 30), (kb > kb0 || kk > 0) ? 1u : 0u);
         mma_commit(&empty[s]);
         if ((kb & 3) == 3) {
@@ -656,11 +663,11 @@ __global__ void __launch_bounds__(128)
   } else if (warp == 2) {
     const int xb0 = z * (p.x_koff / 128);
     const int64_t wr = (int64_t)z * a.w_rblocks + nt;
-    constexpr int kRows = NT < 32 ? 1 : NT / 32;   // of this lane
+    constexpr int kMine = NT < 32 ? 1 : NT / 32;   // rows of this lane
     uint32_t x[4] = {0u, 0u, 0u, 0u}, w;
     auto load = [&](int kb) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
+      for (int i = 0; i < kMine; ++i) {
         const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
         a.xs.get<1>(m < p.M ? m : p.M - 1, xb0 + kb, &x[i]);
       }
@@ -695,13 +702,22 @@ __global__ void __launch_bounds__(128)
   const int rows = (int)(p.M - m0 < NT ? p.M - m0 : NT);
   const int col = warp * 32 + lane;
   const int64_t y0 = m0 * p.y_ld + (int64_t)z * p.y_noff + n0;
+  if constexpr (kRows) {
+    uint32_t r[128];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tmem_ld32(base + q * 32, r + q * 32);
+    tmem_ld_wait();
+    const int64_t at = y0 + col * p.y_ld;   // col: this lane's row of X
+    if (col < rows)   // N is a multiple of 128
+      store_codes128(reinterpret_cast<float*>(r), static_cast<uint8_t*>(p.y) + at, p.y_sf + at / 128);
+  }
   float* part = reinterpret_cast<float*>(sm + L::off_part);   // [row t / SPLIT][rank][128]
   uint32_t to[SPLIT];
 #pragma unroll
   for (int j = 0; j < SPLIT; ++j)
     to[j] = cluster_addr(part + rank * kTileM + col, (uint32_t)j);
 #pragma unroll 1
-  for (int t0 = 0; t0 < rows; t0 += step) {
+  for (int t0 = 0; t0 < rows && !kRows; t0 += step) {
     uint32_t r[step];
     if constexpr (step == 32) tmem_ld32(base + t0, r);
     else tmem_ld16(base + t0, r);
@@ -714,7 +730,7 @@ __global__ void __launch_bounds__(128)
       if constexpr (kSum) {
         // step is a multiple of SPLIT, so t mod SPLIT is i mod SPLIT
         dsmem_st_f32(to[i % SPLIT] + (uint32_t)(t - i % SPLIT) * (kTileM * 4), v);
-      } else if (n0 + col < p.N) {
+      } else if (!kRows && n0 + col < p.N) {
         const int64_t at = y0 + t * p.y_ld + col;
         if (OUT == CSA_BF16) static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
         else static_cast<float*>(p.y)[at] = v;
@@ -728,6 +744,7 @@ __global__ void __launch_bounds__(128)
     // a warp adds one X row's partials, four columns a lane: side by side where
     // Y's rows take 8- or 16-byte stores, else 32 apart
     const bool vec = OUT == kFp8Out || a.y_align >= 16;
+#pragma unroll 2
     for (int k = warp; k * SPLIT + rank < rows; k += 4) {
       float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -743,13 +760,9 @@ __global__ void __launch_bounds__(128)
       }
       const int64_t row = y0 + (int64_t)(k * SPLIT + rank) * p.y_ld;
       if constexpr (OUT == kFp8Out) {   // N, and rows of Y, are multiples of 128
-        float am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
-                                        fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));   // skips NaN
-        if (isinf(am)) {   // rare: the scale from the finite elements
-          drop_infinities<4>(v);
-          am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
-                                    fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));
-        }
+        drop_infinities<4>(v);
+        const float am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
+                                              fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));   // skips NaN
         const uint32_t byte = scale_byte(am);
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row + 4 * lane) =
             codes4(v, byte);
@@ -796,26 +809,25 @@ cudaError_t allow_smem(void (*kernel)(KArgs...), int smem, std::atomic<bool>* do
   return e;
 }
 
-// launch_pdl in clusters of `cluster` CTAs.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(KArgs...), int64_t grid, int threads, size_t smem,
-                            int cluster, cudaStream_t stream, Args&&... args) {
+// A launch in clusters of `cluster` CTAs with programmatic stream serialization.
+struct ClusterLaunch {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-}
+  ClusterLaunch(int64_t grid, int threads, size_t smem, int cluster, cudaStream_t stream) {
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+  }
+};
 
 template <int OUT>
 cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
@@ -832,24 +844,54 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   cudaError_t e = allow_smem(fp8_gemm_kernel<OUT>, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t pairs = sm_count() / 2;
-  return launch_clusters(fp8_gemm_kernel<OUT>, 2 * (a.tiles < pairs ? a.tiles : pairs), kThreads,
-                         smem, 2, stream, mx, mw, a);
+  ClusterLaunch l(2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, smem, 2, stream);
+  return cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<OUT>, mx, mw, a);
 }
 
 template <int NT, int SPLIT, int OUT>
-cudaError_t launch_few(const GemmArgs& a, cudaStream_t stream) {
-  const Fp8GemmParams& p = a.p;
-  CUtensorMap mx, mw;
-  if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, NT) ||
-      !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kTileM))
-    return cudaErrorInvalidValue;
-  const int smem = Few<NT, (SPLIT > 1 || OUT == kFp8Out)>::smem + 1024;
-  auto kernel = fp8_gemm_few_kernel<NT, SPLIT, OUT>;
-  static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = allow_smem(kernel, smem, done);
-  if (e != cudaSuccess) return e;
-  return launch_clusters(kernel, a.tiles * SPLIT, 128, smem, SPLIT, stream, mx, mw, a);
-}
+struct FewKernel {
+  static constexpr bool sum = (SPLIT > 1 || OUT == kFp8Out) && !few_rows_on_m<NT, SPLIT, OUT>;
+  static constexpr int smem = Few<NT, sum>::smem + 1024;
+
+  static cudaError_t allow() {
+    static std::atomic<bool> done[kMaxDevices];
+    return allow_smem(fp8_gemm_few_kernel<NT, SPLIT, OUT>, smem, done);
+  }
+  // Clusters that run at once on the current device (asked once per device): a
+  // cluster lies within a GPC, so there are fewer than the SMs would hold.  The
+  // answer is for one CTA on an SM (74, 33 and 15 clusters of two, four and eight);
+  // with two, odd SMs of a GPC pair up, which makes two more (32 x N x 4096 by
+  // fours: 68 tiles 9.9 us, 72 14.3; by eights: 32 tiles 10.1, 34 14.3).
+  static constexpr int per_sm = 2 * (smem + 1024) <= 233472 ? 2 : 1;
+  static int clusters() {
+    static std::atomic<int> known[kMaxDevices];
+    const int dev = current_device();
+    int n = dev >= 0 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    ClusterLaunch l(SPLIT, 128, smem, SPLIT, nullptr);
+    if (allow() != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fp8_gemm_few_kernel<NT, SPLIT, OUT>, &l.cfg) !=
+            cudaSuccess ||
+        n <= 0) {
+      cudaGetLastError();
+      return per_sm * sm_count() / SPLIT * 3 / 4;
+    }
+    if (per_sm == 2) n = 2 * n + 2;
+    if (dev >= 0) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+  }
+  static cudaError_t launch(const GemmArgs& a, cudaStream_t stream) {
+    const Fp8GemmParams& p = a.p;
+    CUtensorMap mx, mw;
+    if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, NT) ||
+        !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kTileM))
+      return cudaErrorInvalidValue;
+    const cudaError_t e = allow();
+    if (e != cudaSuccess) return e;
+    ClusterLaunch l(a.tiles * SPLIT, 128, smem, SPLIT, stream);
+    return cudaLaunchKernelEx(&l.cfg, fp8_gemm_few_kernel<NT, SPLIT, OUT>, mx, mw, a);
+  }
+};
 
 template <int NT, int OUT>
 cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
@@ -857,22 +899,22 @@ cudaError_t launch_few(GemmArgs& a, cudaStream_t stream) {
   a.m_tiles = (int)((p.M + NT - 1) / NT);
   a.n_tiles = (p.N + kTileM - 1) / kTileM;
   a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
-  // K shares: as many as fit the SMs at once, of two chunks or more unless fewer
-  // than 48 CTAs would run (1 x 4096 x 4096: four shares 4.7 us, eight 5.2; 1 x
-  // 1024 x 4096: four 4.4, eight 3.7)
+  if (a.tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // K shares: as many as run at once (57 x 9216 x 10752, 72 tiles: clusters of four
+  // did not all, 30 us; of two 23), of two chunks or more unless fewer than
+  // 48 CTAs would run (1 x 4096 x 4096: four shares 4.7 us, eight 5.2; 1 x 1024 x
+  // 4096: four 4.4, eight 3.7)
   const int chunks = (a.kb_n + kChunk - 1) / kChunk;
-  const int64_t room = (int64_t)Few<NT, true>::resident * sm_count();
-  int split = 1;
-  while (split < 8 && split * 2 <= chunks && a.tiles * split * 2 <= room &&
-         (split * 4 <= chunks || a.tiles * split < 48))
-    split *= 2;
-  if (a.tiles * split > 0x7fffffffLL) return cudaErrorInvalidValue;
-  switch (split) {
-    case 1: return launch_few<NT, 1, OUT>(a, stream);
-    case 2: return launch_few<NT, 2, OUT>(a, stream);
-    case 4: return launch_few<NT, 4, OUT>(a, stream);
-    default: return launch_few<NT, 8, OUT>(a, stream);
-  }
+  auto more = [&](int split) {
+    return split * 2 <= chunks && (split * 4 <= chunks || a.tiles * split < 48);
+  };
+  if (!more(1) || a.tiles > FewKernel<NT, 2, OUT>::clusters())
+    return FewKernel<NT, 1, OUT>::launch(a, stream);
+  if (!more(2) || a.tiles > FewKernel<NT, 4, OUT>::clusters())
+    return FewKernel<NT, 2, OUT>::launch(a, stream);
+  if (!more(4) || a.tiles > FewKernel<NT, 8, OUT>::clusters())
+    return FewKernel<NT, 4, OUT>::launch(a, stream);
+  return FewKernel<NT, 8, OUT>::launch(a, stream);
 }
 
 template <int OUT>
@@ -887,7 +929,7 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   // x 4096 17.3, 17.7; 512 x 4096 x 4096 16.2, 14.4; 4096 x 2048 x 1024 13.4, 15.2;
   // 2048 x 2048 x 2048 12.5, 11.3).
   const int64_t pairs = tiles(2 * kTileM, kN);
-  if (pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536))
+  if (p.M > 128 && pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536))
     return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
   // Smaller row tiles share the epilogue among more SMs, at the price of reading W
@@ -899,6 +941,7 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   if (p.M <= 32 || (a.kb_n <= 8 && tiles(32, kTileM) <= sms))
     return launch_few<32, OUT>(a, stream);
   const int64_t t128 = tiles(128, kTileM), t64 = tiles(64, kTileM);
+  if (p.M > 64 && OUT == kFp8Out) return launch_few<128, OUT>(a, stream);
   if (p.M <= 64 || t64 <= 32 || (a.kb_n <= 16 && t64 <= sms) ||
       (5 * t128 > 3 * sms && t128 <= sms && t64 <= 2 * sms))
     return launch_few<64, OUT>(a, stream);
