@@ -458,8 +458,8 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  * A row's result does not depend on the other rows' values; it may differ in
  * its last bits between values of M, which choose the split of K.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad out_dtype, negative M or
- * N, K < 1, y_ld < N), CSA_E_UNSUPPORTED (K not a multiple of 16, or M, N, K
- * beyond 2^30), CSA_E_WORKSPACE.
+ * N, K < 1, y_ld < N), CSA_E_UNSUPPORTED (K not a multiple of 16, M or N
+ * beyond 2^30, K beyond 2^26), CSA_E_WORKSPACE.
  */
 csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const void* x_codes,
                       const void* x_scales, const void* w_codes, const void* w_scales, void* y,

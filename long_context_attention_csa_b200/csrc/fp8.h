@@ -12,6 +12,7 @@ namespace csa {
 constexpr int kFp8MaxNormDim = 32768;   // columns rmsnorm_fp8 holds in registers
 
 constexpr int64_t kFp8MaxDim = 1 << 30;  // rows and columns of a product: tile ends fit 32 bits
+constexpr int64_t kFp8MaxK = 1 << 26;    // a tile's sum ends well within a bounded wait
 
 struct NormParams {
   int64_t T;

@@ -392,16 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         mma_commit_pair(tfull);
       }
-      mma_commit_pair(drain);
+      mma_commit_one_of_pair(drain);
+      mbar_wait(drain, 0);
     }
-    __syncwarp();
-    mbar_wait(drain, 0);
   } else if (warp == 2) {
     // scale tiles: a lane holds rows lane, lane + 32, ... of X; W's rows all
-    // carry their 128-row block's word.  The fence and the arrival at rank 0
-    // take about as long as a chunk's MMAs (2400 of 2048 cycles), so four chunks
-    // are handed over at once: 281 -> 253 us for 9472 x 2048 x 16384 with the
-    // loads grouped alone.
+    // carry their 128-row block's word.  The loads, and the fence and arrival at
+    // rank 0 (2400 cycles), each take longer than a chunk's MMAs (2048), so four
+    // chunks go together (9472 x 2048 x 16384: one at a time 281 us, loads by fours
+    // 253, both 225).
     uint32_t gr = 0;
     bool ok = true;
     for (int64_t u = first; u < a.tiles && ok; u += step) {

@@ -66,6 +66,7 @@ def matmul(L, out=BF16, M=4, N=8, K=256, x=PTR, xs=PTR, w=PTR, ws_=PTR, y=PTR, l
     (dict(y=None), ARG), (dict(x=MIS), ARG), (dict(w=MIS), ARG), (dict(y=ctypes.c_void_p(4097)), ARG),
     (dict(out=F32, y=ctypes.c_void_p(4098)), ARG), (dict(K=250), UNSUPPORTED),
     (dict(M=1 << 31), UNSUPPORTED), (dict(N=1 << 31, ld=1 << 31), UNSUPPORTED),
+    (dict(K=(1 << 26) + 16), UNSUPPORTED),
     (dict(ws=None), WORKSPACE), (dict(ws_bytes=255), WORKSPACE),
     (dict(M=0), 0), (dict(N=0, ld=0), 0),
 ])
