@@ -609,22 +609,35 @@ def measure_projection(dev, steps: int, warmup: int, flush, ws_n: int, cpu: bool
     def run():
         csa.grouped_output_projection(x["o"], x["w_group"], x["w_out"], y=y, ws=ws)
 
-    for _ in range(warmup):
-        run()
-    torch.cuda.synchronize()
-    evs = []
-    for _ in range(steps):
-        flush()
-        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        e0.record()
-        run()
-        e1.record()
-        evs.append((e0, e1))
-    torch.cuda.synchronize()
-    st, d = csa.csa_check_status(ws)
-    if st:
-        raise RuntimeError(f"projection: device status {st}/{d}")
-    ms = allmax(float(np.mean([a.elapsed_time(b) for a, b in evs])), ws_n)
+    def timed(call, work):
+        for _ in range(warmup):
+            call()
+        torch.cuda.synchronize()
+        evs = []
+        for _ in range(steps):
+            flush()
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            call()
+            e1.record()
+            evs.append((e0, e1))
+        torch.cuda.synchronize()
+        st, d = csa.csa_check_status(work)
+        if st:
+            raise RuntimeError(f"projection: device status {st}/{d}")
+        return allmax(float(np.mean([a.elapsed_time(b) for a, b in evs])), ws_n)
+
+    ms = timed(run, ws)
+    # the same projection in FP8: o quantized in the call, weights once before
+    kg = w.H // p["g"] * w.c
+    wg, wgs = csa.fp8_quantize(x["w_group"].view(p["g"] * p["d_g"], kg), 128)
+    wo, wos = csa.fp8_quantize(x["w_out"], 128)
+    ws8 = csa.workspace(csa.csa_workspace_bytes(csa.CSA_OP_OUT_PROJ_FP8, 1, 1, w.T, w.H, w.c,
+                                                p["g"] * p["d_g"]), dev)
+    ms8 = timed(lambda: csa.grouped_output_projection_fp8(
+        x["o"], wg.view(p["g"], p["d_g"], kg), wgs.view(p["g"], p["d_g"] // 128, kg // 128),
+        wo, wos, y=y, ws=ws8), ws8)
+    del wg, wgs, wo, wos, ws8
     fl = 2.0 * w.T * (w.H * w.c * p["d_g"] + p["g"] * p["d_g"] * p["d"])
     _, bf16, src = peaks()
     achieved = fl / (ms * 1e-3) / 1e12
@@ -637,7 +650,11 @@ def measure_projection(dev, steps: int, warmup: int, flush, ws_n: int, cpu: bool
                         "achieved": achieved, "peak": bf16, "unit": "TFLOP/s",
                         "frac": achieved / bf16, "algorithmic_flops_per_call": fl,
                         "peak_source": f"{src} bf16 burst (MEASURED_PEAKS.json)"
-                        if src == "measured" else "fallback 1.59 PFLOP/s"}}
+                        if src == "measured" else "fallback 1.59 PFLOP/s"},
+           "fp8": {"value": w.T * ws_n / (ms8 * 1e-3), "unit": "tokens/s", "ms": ms8,
+                   "tflops": fl / (ms8 * 1e-3) / 1e12,
+                   "format": "E4M3, a power-of-two scale per 128 columns (activations) or "
+                             "128 x 128 block (weights)"}}
     if cpu:
         import oracle
 

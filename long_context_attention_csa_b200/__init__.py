@@ -444,10 +444,10 @@ _FP8_TYPES = frozenset((_E4M3, _E8M0, torch.uint8))
 _FLOATS = {torch.bfloat16: CSA_BF16, torch.float32: CSA_F32}
 
 
-def _launch(idx, stream, what, fn, *args):
-    """fn(*args, stream) on device idx's current stream unless one is given,
-    with the device current while it launches."""
-    raw = torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream
+def _launch(idx, what, fn, *args):
+    """fn(*args, stream) on device idx's current stream, with the device current
+    while it launches."""
+    raw = torch._C._cuda_getCurrentRawStream(idx)
     if idx == torch._C._cuda_getDevice():
         st = fn(*args, raw)
     else:
@@ -455,6 +455,15 @@ def _launch(idx, stream, what, fn, *args):
             st = fn(*args, raw)
     if st != CSA_OK:
         raise CSAError(st, what)
+
+
+def _on(stream, x, call, *args):
+    """call(*args) with `stream`, which is one of x's device, current: what the
+    call allocates and fills is then ordered with what it launches."""
+    if stream.device != x.device:
+        _refuse(f"stream of {stream.device}, tensors on {x.device}")
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _refuse(what: str):
@@ -526,6 +535,8 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
     activations: codes [..., d] float8_e4m3fn and scales [..., ceil(d/128)]
     float8_e8m0fnu.  With a residual also returns x + residual (in ``sum_out``,
     which may be x or residual itself)."""
+    if stream is not None:
+        return _on(stream, x, rmsnorm_fp8, x, residual, gain, eps, sum_out, codes, scales)
     idx, shape, d = _cuda_rows(x, "rmsnorm_fp8")
     dt = x.dtype
     x_ld = _row_stride(x, shape, dt, idx, "x")
@@ -549,7 +560,7 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
         pg = gain.data_ptr()
     codes, scales, pc, psc = _fp8_pair(x, shape, shape[:-1] + ((d + 127) // 128,), idx, codes,
                                        scales)
-    _launch(idx, stream, "rmsnorm_fp8", lib().rmsnorm_fp8, _FLOATS.get(dt, -1), x.numel() // d, d,
+    _launch(idx, "rmsnorm_fp8", lib().rmsnorm_fp8, _FLOATS.get(dt, -1), x.numel() // d, d,
             x.data_ptr(), x_ld, pr, r_ld, pg, eps, ps, s_ld, pc, psc)
     return (codes, scales) if sum_out is None else (codes, scales, sum_out)
 
@@ -557,6 +568,8 @@ def rmsnorm_fp8(x, residual=None, gain=None, eps: float = 1e-6, sum_out=None, co
 def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
     """FP8 activations of x [..., d] (block_rows 1), or FP8 weights of x
     [rows, d] (block_rows 128): codes and scales [ceil(rows/128), ceil(d/128)]."""
+    if stream is not None:
+        return _on(stream, x, fp8_quantize, x, block_rows, codes, scales)
     idx, shape, d = _cuda_rows(x, "fp8_quantize")
     dt = x.dtype
     ld = _row_stride(x, shape, dt, idx, "x")
@@ -567,7 +580,7 @@ def fp8_quantize(x, block_rows: int = 1, codes=None, scales=None, stream=None):
     else:
         _refuse("fp8_quantize: weights are [rows, d]")
     codes, scales, pc, ps = _fp8_pair(x, shape, sshape, idx, codes, scales)
-    _launch(idx, stream, "fp8_quantize", lib().fp8_quantize, _FLOATS.get(dt, -1), x.numel() // d,
+    _launch(idx, "fp8_quantize", lib().fp8_quantize, _FLOATS.get(dt, -1), x.numel() // d,
             d, x.data_ptr(), ld, block_rows, pc, ps)
     return codes, scales
 
@@ -578,6 +591,9 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
     and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
     bf16 or fp32.  ``y``, whose dtype then counts, may be a two-dimensional
     column slice of a wider buffer."""
+    if stream is not None:
+        return _on(stream, x_codes, fp8_matmul, x_codes, x_scales, w_codes, w_scales, out_dtype, y,
+                   ws)
     idx, shape, K = _cuda_rows(x_codes, "fp8_matmul")
     lead, nb = shape[:-1], (K + 127) // 128
     wshape = w_codes.shape
@@ -595,7 +611,7 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
         out_dtype = y.dtype
         y_ld = _row_stride(y, lead + (N,), out_dtype, idx, "y")
     pws_, nws, ws = _ws(ws, 256, idx)
-    _launch(idx, stream, "fp8_matmul", lib().fp8_matmul, _FLOATS.get(out_dtype, -1),
+    _launch(idx, "fp8_matmul", lib().fp8_matmul, _FLOATS.get(out_dtype, -1),
             x_codes.numel() // K, N, K, px, pxs, pw, pws, y.data_ptr(), y_ld, pws_, nws)
     return y
 
@@ -605,6 +621,9 @@ def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scale
     """Grouped output projection in FP8: o [T, H, c] (bf16 or fp32), w_group
     [g, d_g, (H/g) c] and w_out [d, g d_g] FP8 weights (the scales of w_group
     [g, d_g/128, (H/g) c/128]) -> y [T, d] bf16."""
+    if stream is not None:
+        return _on(stream, o, grouped_output_projection_fp8, o, w_group, w_group_scales, w_out,
+                   w_out_scales, y, ws)
     idx, shape, c = _cuda_rows(o, "grouped_output_projection_fp8")
     if len(shape) != 3 or w_group.dim() != 3 or w_out.dim() != 2 or not o.is_contiguous():
         _refuse("o: contiguous [T, H, c], w_group: [g, d_g, k], w_out: [d, g d_g]")
@@ -628,6 +647,6 @@ def grouped_output_projection_fp8(o, w_group, w_group_scales, w_out, w_out_scale
     need = 0 if ws is not None else csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dt, 1, T, H, c,
                                                         g * dg)
     pws, nws, ws = _ws(ws, need, idx)
-    _launch(idx, stream, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
+    _launch(idx, "grouped_output_projection_fp8", lib().grouped_output_projection_fp8,
             dt, T, H, c, g, dg, d, o.data_ptr(), pg, pgs, po, pos, y.data_ptr(), pws, nws)
     return y

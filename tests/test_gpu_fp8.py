@@ -457,6 +457,30 @@ def test_other_streams_and_captured_graphs():
     assert all(torch.equal(a, b) for a, b in zip(out, want)) and torch.equal(out_p, want_p)
 
 
+def test_stream_argument():
+    """Calls given a stream while the current one is busy: what they allocate and
+    zero belongs to that stream."""
+    x, r = normal((300, 2048), torch.bfloat16, 1), normal((300, 2048), torch.bfloat16, 2)
+    wc, wsc = csa.fp8_quantize(normal((1024, 2048), torch.float32, 3, 2048 ** -0.5), 128)
+    p = proj_inputs(300, 8, 256, 2, 512, 768, 4)
+    want = csa.rmsnorm_fp8(x, r)
+    want_y, want_p = csa.fp8_matmul(want[0], want[1], wc, wsc), csa.grouped_output_projection_fp8(*p)
+    big = torch.randn(8192, 8192, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        (big @ big).mul_(0)                      # the current stream is busy
+        got = csa.rmsnorm_fp8(x, r, stream=side)
+        c, s = csa.fp8_quantize(x, stream=side)
+        y = csa.fp8_matmul(got[0], got[1], wc, wsc, stream=side)
+        o = csa.grouped_output_projection_fp8(*p, stream=side)
+        side.synchronize()
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(got, want))
+        assert torch.equal(y, want_y) and torch.equal(o, want_p)
+        assert torch.equal(bits(c), bits(csa.fp8_quantize(x)[0]))
+    torch.cuda.synchronize()
+
+
 def test_two_streams_at_once():
     cases = [operands(60, 700, 2048, 30), operands(900, 600, 1024, 31)]
     want = [csa.fp8_matmul(*c) for c in cases]
