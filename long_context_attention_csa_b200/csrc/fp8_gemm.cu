@@ -196,40 +196,51 @@ static_assert(kGroup * kChunk == 16, "a group is what aligned rows load at once"
 
 // Thirty-two columns of a warp's `rows` rows (lane = row), `n` of them inside Y,
 // whose rows start anywhere: through shared memory, so that a store's lanes lie
-// side by side.
+// side by side, a row a store (two rows of bf16 pairs, where rows start on 4-byte
+// boundaries: 4097 x 4098 x 1024 35.6 us, this way 28.7).  One warp a scheduler
+// runs this, so its instructions count: sixteen a row were 52 us of a 3412 x 5471
+// x 944 product.
+template <bool WHOLE, typename E>
+__device__ __forceinline__ void store_rows32(E* dst, int64_t ld, const uint32_t* stage, int rows,
+                                             bool in, int shift) {
+#pragma unroll
+  for (int q = 0; q < 32; ++q, dst += ld) {
+    const uint32_t w = stage[q * kStagePitch] >> shift;
+    if (in && (WHOLE || q < rows)) *dst = (E)w;
+  }
+}
+
 template <int OUT>
 __device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, const uint32_t* r,
-                                             int rows, int n, uint32_t* stage,
-                                             int lane) {
-  const int half = lane >> 4, c = lane & 15;
+                                             int rows, int n, uint32_t* stage, int lane) {
+  __syncwarp();
   if constexpr (OUT == CSA_BF16) {
-    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       stage[lane * kStagePitch + i] =
           pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
     __syncwarp();
-    // a row a store, a column a lane (two rows of pairs, where rows start on 4-byte
-    // boundaries: 4097 x 4098 x 1024 35.6 us, this way 28.7)
-    bf16* dst = static_cast<bf16*>(y) + at + lane;
-#pragma unroll 8
-    for (int q = 0; q < 32; ++q, dst += ld) {
-      const uint32_t w = stage[q * kStagePitch + (lane >> 1)];
-      if (q < rows && lane < n)
-        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)((lane & 1) ? w >> 16 : w);
-    }
+    uint16_t* dst = static_cast<uint16_t*>(y) + at + lane;
+    const uint32_t* src = stage + (lane >> 1);
+    const int shift = (lane & 1) * 16;
+    if (rows >= 32) store_rows32<true>(dst, ld, src, rows, lane < n, shift);
+    else store_rows32<false>(dst, ld, src, rows, lane < n, shift);
   } else {
+    // sixteen columns at a time: the warp's halves take even and odd rows
+    const int half = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      __syncwarp();
+      if (h) __syncwarp();
 #pragma unroll
       for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = r[16 * h + i];
       __syncwarp();
       uint32_t* dst = static_cast<uint32_t*>(y) + at + half * ld + 16 * h + c;
-#pragma unroll 8
-      for (int q = half; q < 32; q += 2, dst += 2 * ld) {
-        const uint32_t w = stage[q * kStagePitch + c];
-        if (q < rows && 16 * h + c < n) *dst = w;
+      const uint32_t* src = stage + half * kStagePitch + c;
+      const bool in = 16 * h + c < n;
+#pragma unroll
+      for (int q = 0; q < 32; q += 2, dst += 2 * ld) {
+        const uint32_t w = src[q * kStagePitch];
+        if (in && q + half < rows) *dst = w;
       }
     }
   }
@@ -715,6 +726,10 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int j = 0; j < SPLIT; ++j)
     to[j] = cluster_addr(part + rank * kTileM + col, (uint32_t)j);
+  constexpr int kElem = OUT == CSA_BF16 ? 2 : 4;
+  const bool inside = n0 + col < p.N;   // this lane's column, where it goes straight to Y
+  const int64_t pitch = p.y_ld * kElem;
+  char* dst = static_cast<char*>(p.y) + (y0 + col) * kElem;
 #pragma unroll 1
   for (int t0 = 0; t0 < rows && !kRows; t0 += step) {
     uint32_t r[step];
@@ -725,14 +740,16 @@ __global__ void __launch_bounds__(128)
     for (int i = 0; i < step; ++i) {
       const int t = t0 + i;
       const float v = __uint_as_float(r[i]);
-      if (t >= rows) continue;
       if constexpr (kSum) {
+        if (t >= rows) continue;
         // step is a multiple of SPLIT, so t mod SPLIT is i mod SPLIT
         dsmem_st_f32(to[i % SPLIT] + (uint32_t)(t - i % SPLIT) * (kTileM * 4), v);
-      } else if (!kRows && n0 + col < p.N) {
-        const int64_t at = y0 + t * p.y_ld + col;
-        if (OUT == CSA_BF16) static_cast<bf16*>(p.y)[at] = __float2bfloat16_rn(v);
-        else static_cast<float*>(p.y)[at] = v;
+      } else if constexpr (!kRows) {
+        if (inside && t < rows) {
+          if (OUT == CSA_BF16) *reinterpret_cast<bf16*>(dst) = __float2bfloat16_rn(v);
+          else *reinterpret_cast<float*>(dst) = v;
+        }
+        dst += pitch;
       }
     }
   }
