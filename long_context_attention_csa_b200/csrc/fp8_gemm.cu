@@ -171,7 +171,7 @@ __device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t*
 //   warp 0     TMA producer, a six-slot ring of K blocks (16 + 16 KB); both CTAs'
 //              loads complete on rank 0's barrier
 //   warp 1     TMEM owner; rank 0: single-thread MMA issuer for the pair
-//   warp 2     scale tiles in shared memory
+//   warps 2-3  scale tiles in shared memory, by turns
 //   warps 4-7  epilogue, thread = row
 // The two 256-column accumulators and the scales' 24 columns do not fit 512, so
 // the accumulators share 24 columns: the epilogue reads those first and only
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1, tiles = (uint32_t)a.tiles;
   const Fp8GemmParams& p = a.p;
 
   if (threadIdx.x == 0) {
@@ -298,12 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  auto tile_of = [&](int64_t u, int& z, int64_t& m0, int& n0) {
-    const int nt = (int)(u % a.n_tiles);
-    const int64_t r = u / a.n_tiles;
-    m0 = (r % a.m_tiles) * (2 * kTileM) + rank * kTileM;   // this CTA's rows
-    z = (int)(r / a.m_tiles);
-    n0 = nt * kN;
+  auto tile_of = [&](uint32_t u, int& z, int64_t& m0, int& n0) {
+    const uint32_t r = u / (uint32_t)a.n_tiles, q = r / (uint32_t)a.m_tiles;
+    m0 = (int64_t)(r - q * a.m_tiles) * (2 * kTileM) + rank * kTileM;   // this CTA's rows
+    z = (int)q;
+    n0 = (int)(u - r * a.n_tiles) * kN;
   };
   auto give_up = [&](unsigned where) {
     *abort_flag = 1;
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t u = first; u < a.tiles && ok; u += step) {
+      for (uint32_t u = first; u < tiles && ok; u += step) {
         int z, n0;
         int64_t m0;
         tile_of(u, z, m0, n0);
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0 && elect_one()) {
       uint32_t it = 0, ch = 0, gr = 0, n = 0;   // stages, chunks, groups, tiles
       bool landed = false;                      // stage `it` is known to have landed
-      for (int64_t u = first; u < a.tiles; u += step, ++n) {
+      for (uint32_t u = first; u < tiles; u += step, ++n) {
         if (*abort_flag || (n > 0 && !mbar_wait(tfree, (n - 1) & 1u))) {
           give_up(0x802u);
           break;
@@ -406,15 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_one_of_pair(drain);
       mbar_wait(drain, 0);
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // scale tiles: a lane holds rows lane, lane + 32, ... of X; W's rows all
     // carry their 128-row block's word.  The loads, and the fence and arrival at
     // rank 0 (2400 cycles), each take longer than a chunk's MMAs (2048), so four
     // chunks go together (9472 x 2048 x 16384: one at a time 281 us, loads by fours
-    // 253, both 225).
+    // 253, both 225) and two warps take turns.
     uint32_t gr = 0;
     bool ok = true;
-    for (int64_t u = first; u < a.tiles && ok; u += step) {
+    for (uint32_t u = first; u < tiles && ok; u += step) {
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
@@ -422,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t wr = (int64_t)z * a.w_rblocks + n0 / 128;
       const bool second = n0 / 128 + 1 < a.w_rblocks;
       for (int kb = 0; kb < a.kb_n; kb += kGroup * kChunk, ++gr) {
+        if ((gr & 1u) != (uint32_t)(warp & 1)) continue;   // the other warp's
         uint32_t x[4][kGroup], w[2][kGroup];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_cluster_exec(free_bar);
     };
     uint32_t n = 0;
-    for (int64_t u = first; u < a.tiles; u += step, ++n) {
+    for (uint32_t u = first; u < tiles; u += step, ++n) {
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
@@ -492,22 +492,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                            p.y_sf + (at + c0) / 128);
         }
       } else {
+        // thirty-two columns at a time, the shared ones first, the next ones on
+        // their way from TMEM while these are stored
+        const int64_t mw = m0 + quarter * 32;   // this warp's first row
+        const int rows = (int)(p.M - mw < 32 ? p.M - mw : 32);
+        auto col = [&](int i) { return odd ? 32 * i : kN - 32 - 32 * i; };
+        auto store = [&](int cc, const uint32_t* r) {
+          const int n_in = p.N - n0 - cc;
+          if (n_in <= 0) return;
+          if (a.y_align < 16)
+            store_tile32<OUT>(p.y, at - lane * p.y_ld + cc, p.y_ld, r, rows, n_in, stage, lane);
+          else if (live)
+            store_row32<OUT>(p.y, at + cc, r, n_in, a.y_align >= 32);
+        };
+        uint32_t r[2][32];
+        tmem_ld32(base + col(0), r[0]);
+        tmem_ld_wait();
+        release();
 #pragma unroll 1
-        for (int i = 0; i < kN / 32; ++i) {
-          const int cc = odd ? 32 * i : kN - 32 - 32 * i;   // the shared columns first
-          uint32_t r[32];
-          tmem_ld32(base + cc, r);
+        for (int i = 0; i < kN / 32; i += 2) {
+          tmem_ld32(base + col(i + 1), r[1]);
+          store(col(i), r[0]);
           tmem_ld_wait();
-          if (i == 0) release();
-          if (n0 + cc >= p.N) continue;
-          if (a.y_align >= 16) {
-            if (live) store_row32<OUT>(p.y, at + cc, r, p.N - n0 - cc, a.y_align >= 32);
-          } else {
-            const int64_t m = m0 + quarter * 32;   // this warp's first row
-            store_tile32<OUT>(p.y, m * p.y_ld + (int64_t)z * p.y_noff + n0 + cc, p.y_ld, r,
-                              (int)(p.M - m < 32 ? p.M - m : 32), p.N - n0 - cc, stage,
-                              lane);
-          }
+          if (i + 2 < kN / 32) tmem_ld32(base + col(i + 2), r[0]);
+          store(col(i + 1), r[1]);
+          tmem_ld_wait();
         }
       }
     }
@@ -851,6 +860,7 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   a.m_tiles = (int)((p.M + 2 * kTileM - 1) / (2 * kTileM));
   a.n_tiles = (p.N + kN - 1) / kN;
   a.tiles = (int64_t)p.Z * a.m_tiles * a.n_tiles;
+  if (a.tiles > 0x7fffffffLL) return cudaErrorInvalidValue;   // no memory holds such a Y
   CUtensorMap mx, mw;
   if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, kTileM) ||
       !make_map_u8_3d(&mw, p.w, (uint64_t)p.K, (uint64_t)p.N, (uint64_t)p.Z, kBK, kN / 2))
