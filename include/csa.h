@@ -11,6 +11,8 @@
  *     group, rate 1/m'), followed by RMSNorm and partial RoPE;
  *   - indexer_scores_topk: the lightning-indexer score
  *     I[t,s] = sum_h w[t,h] ReLU(q_I[t,h] . K_I[s]) and a causal per-query top-k;
+ *   - rmsnorm_fp8, fp8_quantize, fp8_matmul, grouped_output_projection_fp8: the
+ *     layer's projections in 8 bits;
  *   - sparse_mqa_attn / dense_hca_attn: multi-query attention in which each
  *     compressed entry is both key and value, over the selected entries (CSA)
  *     or all visible entries (HCA), plus a sliding window of per-token rows and

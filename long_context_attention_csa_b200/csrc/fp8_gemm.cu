@@ -15,8 +15,12 @@
 // (r div 32)) and tcgen05.cp brings it into TMEM, two chunks deep.
 //
 // Two kernels.  fp8_gemm_kernel: many rows, X rows on the MMA's M, 256 columns
-// on N, persistent.  fp8_gemm_few_kernel: few rows, where the bytes of W are
-// the bound: W rows on M, the few X rows on N, K split over a cluster.
+// on N, persistent.  Bound by the tensor cores and, back to back, by the chip's
+// power: 8192 x 8192 x 4096 to bf16 in 190 us alone (2.9 PFLOP/s), 216-223 us back
+// to back (2.5 PFLOP/s at 1.3 GHz).
+// fp8_gemm_few_kernel: few rows, where the bytes of W are the bound: W rows on M,
+// the few X rows on N, K split over a cluster.  1 x 8192 x 4096 in 8.4 us, 32 rows
+// in 9.3 (W's 33.6 MB take 5 us of it, at the copy rate).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
