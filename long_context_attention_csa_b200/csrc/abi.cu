@@ -433,8 +433,11 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
   p.y = y;
   p.y_ld = y_ld;
   p.status = status_word(ws);
-  g_launches.fetch_add(1);
-  return cuda_status(launch_fp8_gemm(p, S(stream)));
+  unsigned long long n = 0;
+  p.launches = &n;
+  const cudaError_t e = launch_fp8_gemm(p, S(stream));
+  g_launches.fetch_add(n);
+  return cuda_status(e);
 }
 
 // Workspace of grouped_output_projection_fp8: past the status word the codes
@@ -467,7 +470,7 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   uint8_t* vs = vc + up256((size_t)T * gd);
   cudaError_t e = launch_fp8_quantize(dtype, o, hc, T, (int)hc, 1, oc, os, S(stream));
   if (e != cudaSuccess) return CSA_E_CUDA;
-  g_launches.fetch_add(1);
+  unsigned long long n = 1;
   Fp8GemmParams p{};
   p.M = T;
   p.N = d_g;
@@ -485,9 +488,8 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   p.y_ld = gd;
   p.y_noff = d_g;
   p.status = status_word(ws);
+  p.launches = &n;
   e = launch_fp8_gemm(p, S(stream));
-  if (e != cudaSuccess) return CSA_E_CUDA;
-  g_launches.fetch_add(1);
   p.N = d;
   p.K = p.x_cols = (int)gd;
   p.Z = 1;
@@ -499,8 +501,8 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   p.out = CSA_BF16;
   p.y = y;
   p.y_ld = d;
-  e = launch_fp8_gemm(p, S(stream));
-  if (e == cudaSuccess) g_launches.fetch_add(1);
+  if (e == cudaSuccess) e = launch_fp8_gemm(p, S(stream));
+  g_launches.fetch_add(n);
   return cuda_status(e);
 }
 

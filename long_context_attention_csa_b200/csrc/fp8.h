@@ -72,6 +72,7 @@ struct Fp8GemmParams {
   int64_t y_ld;
   int y_noff;              // per z
   unsigned* status;
+  unsigned long long* launches;   // counted up
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmParams& p, cudaStream_t stream);
 

@@ -89,7 +89,8 @@ struct ScaleRows {
 
 struct GemmArgs {
   Fp8GemmParams p;
-  int kb_n;              // scale blocks (stages) of K
+  int kb_first, kb_n;    // scale blocks (stages) of K that this launch takes
+  bool add;              // onto what Y holds (float32)
   ScaleRows xs, ws;      // scales of X and of all W
   int w_rblocks;         // scale block rows of one W
   int y_align;           // 32, 16 or 1: the boundaries that rows of Y start on
@@ -138,8 +139,8 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool s
 // Thirty-two consecutive values of one row that starts on a 16-byte boundary (32
 // with `sectors`), `n` of them inside Y.
 template <int OUT>
-__device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t* r, int n,
-                                            bool sectors) {
+__device__ __forceinline__ void store_row32(void* y, int64_t at, uint32_t* r, int n, bool sectors,
+                                            bool add) {
   if constexpr (OUT == CSA_BF16) {
     bf16* dst = static_cast<bf16*>(y) + at;
     if (n >= 32) {
@@ -155,6 +156,11 @@ __device__ __forceinline__ void store_row32(void* y, int64_t at, const uint32_t*
     }
   } else {
     float* dst = static_cast<float*>(y) + at;
+    if (add) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) r[i] = __float_as_uint(dst[i] + __uint_as_float(r[i]));
+    }
     if (n >= 32) {
       store_words<32>(dst, r, sectors);
     } else {
@@ -216,7 +222,8 @@ __device__ __forceinline__ void store_rows32(E* dst, int64_t ld, const uint32_t*
 
 template <int OUT>
 __device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, const uint32_t* r,
-                                             int rows, int n, uint32_t* stage, int lane) {
+                                             int rows, int n, bool add, uint32_t* stage,
+                                             int lane) {
   __syncwarp();
   if constexpr (OUT == CSA_BF16) {
 #pragma unroll
@@ -238,13 +245,13 @@ __device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, co
 #pragma unroll
       for (int i = 0; i < 16; ++i) stage[lane * kStagePitch + i] = r[16 * h + i];
       __syncwarp();
-      uint32_t* dst = static_cast<uint32_t*>(y) + at + half * ld + 16 * h + c;
+      float* dst = static_cast<float*>(y) + at + half * ld + 16 * h + c;
       const uint32_t* src = stage + half * kStagePitch + c;
       const bool in = 16 * h + c < n;
 #pragma unroll
       for (int q = 0; q < 32; q += 2, dst += 2 * ld) {
-        const uint32_t w = src[q * kStagePitch];
-        if (in && q + half < rows) *dst = w;
+        const float w = __uint_as_float(src[q * kStagePitch]);
+        if (in && q + half < rows) *dst = add ? *dst + w : w;
       }
     }
   }
@@ -331,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
           const uint32_t bar = cluster_addr(&full[s], 0);
           uint8_t* dst = sm + s * kStage;
-          tma_load_3d_pair(dst, &map_x, bar, z * p.x_koff + kb * kBK, (int32_t)m0, 0);
-          tma_load_3d_pair(dst + kTileA, &map_w, bar, kb * kBK,
-                           n0 + (int)rank * (kN / 2), z);
+          const int k = (a.kb_first + kb) * kBK;
+          tma_load_3d_pair(dst, &map_x, bar, z * p.x_koff + k, (int32_t)m0, 0);
+          tma_load_3d_pair(dst + kTileA, &map_w, bar, k, n0 + (int)rank * (kN / 2), z);
           ++it;
         }
       }
@@ -421,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
-      const int xb0 = z * (p.x_koff / 128);
+      const int xb0 = z * (p.x_koff / 128) + a.kb_first;
       const int64_t wr = (int64_t)z * a.w_rblocks + n0 / 128;
       const bool second = n0 / 128 + 1 < a.w_rblocks;
       for (int kb = 0; kb < a.kb_n; kb += kGroup * kChunk, ++gr) {
@@ -432,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
           a.xs.get<kGroup>(m < p.M ? m : p.M - 1, xb0 + kb, x[i]);
         }
-        a.ws.get<kGroup>(wr, kb, w[0]);
-        a.ws.get<kGroup>(second ? wr + 1 : wr, kb, w[1]);
+        a.ws.get<kGroup>(wr, a.kb_first + kb, w[0]);
+        a.ws.get<kGroup>(second ? wr + 1 : wr, a.kb_first + kb, w[1]);
         const uint32_t slot = gr % kSfSlots;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[slot],
                                                                ((gr / kSfSlots) & 1u) ^ 1u));
@@ -501,13 +508,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t mw = m0 + quarter * 32;   // this warp's first row
         const int rows = (int)(p.M - mw < 32 ? p.M - mw : 32);
         auto col = [&](int i) { return odd ? 32 * i : kN - 32 - 32 * i; };
-        auto store = [&](int cc, const uint32_t* r) {
+        auto store = [&](int cc, uint32_t* r) {
           const int n_in = p.N - n0 - cc;
           if (n_in <= 0) return;
           if (a.y_align < 16)
-            store_tile32<OUT>(p.y, at - lane * p.y_ld + cc, p.y_ld, r, rows, n_in, stage, lane);
+            store_tile32<OUT>(p.y, at - lane * p.y_ld + cc, p.y_ld, r, rows, n_in, a.add,
+                              stage, lane);
           else if (live)
-            store_row32<OUT>(p.y, at + cc, r, n_in, a.y_align >= 32);
+            store_row32<OUT>(p.y, at + cc, r, n_in, a.y_align >= 32, a.add);
         };
         uint32_t r[2][32];
         tmem_ld32(base + col(0), r[0]);
@@ -638,8 +646,9 @@ __global__ void __launch_bounds__(128)
         }
         mbar_arrive_expect_tx(&full[s], L::stage);
         uint8_t* dst = sm + s * L::stage;
-        tma_load_3d(dst, &map_w, &full[s], kb * kBK, n0, z);
-        tma_load_3d(dst + kTileA, &map_x, &full[s], z * p.x_koff + kb * kBK, (int32_t)m0, 0);
+        const int k = (a.kb_first + kb) * kBK;
+        tma_load_3d(dst, &map_w, &full[s], k, n0, z);
+        tma_load_3d(dst + kTileA, &map_x, &full[s], z * p.x_koff + k, (int32_t)m0, 0);
         ++it;
       }
       for (uint32_t i = it > L::stages ? it - L::stages : 0; i < it; ++i)
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(128)
       mma_commit(done);
     }
   } else if (warp == 2) {
-    const int xb0 = z * (p.x_koff / 128);
+    const int xb0 = z * (p.x_koff / 128) + a.kb_first;
     const int64_t wr = (int64_t)z * a.w_rblocks + nt;
     constexpr int kMine = NT < 32 ? 1 : NT / 32;   // rows of this lane
     uint32_t x[4] = {0u, 0u, 0u, 0u}, w;
@@ -694,7 +703,7 @@ __global__ void __launch_bounds__(128)
         const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
         a.xs.get<1>(m < p.M ? m : p.M - 1, xb0 + kb, &x[i]);
       }
-      a.ws.get<1>(wr, kb, &w);
+      a.ws.get<1>(wr, a.kb_first + kb, &w);
     };
     load(kb0);
     uint32_t ch = 0;
@@ -732,7 +741,8 @@ __global__ void __launch_bounds__(128)
     tmem_ld_wait();
     const int64_t at = y0 + col * p.y_ld;   // col: this lane's row of X
     if (col < rows)   // N is a multiple of 128
-      store_codes128(reinterpret_cast<float*>(r), static_cast<uint8_t*>(p.y) + at, p.y_sf + at / 128);
+      store_codes128(reinterpret_cast<float*>(r), static_cast<uint8_t*>(p.y) + at,
+                     p.y_sf + at / 128);
   }
   float* part = reinterpret_cast<float*>(sm + L::off_part);   // [row t / SPLIT][rank][128]
   uint32_t to[SPLIT];
@@ -760,7 +770,7 @@ __global__ void __launch_bounds__(128)
       } else if constexpr (!kRows) {
         if (inside && t < rows) {
           if (OUT == CSA_BF16) *reinterpret_cast<bf16*>(dst) = __float2bfloat16_rn(v);
-          else *reinterpret_cast<float*>(dst) = v;
+          else *reinterpret_cast<float*>(dst) = a.add ? *reinterpret_cast<float*>(dst) + v : v;
         }
         dst += pitch;
       }
@@ -811,6 +821,13 @@ __global__ void __launch_bounds__(128)
           }
         } else {
           float* dst = static_cast<float*>(p.y) + row;
+          if (a.add) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = vec ? 4 * lane + i : lane + 32 * i;
+              if (c < n) v[i] += dst[c];
+            }
+          }
           if (whole) store_vec(dst + 4 * lane, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -858,6 +875,29 @@ struct ClusterLaunch {
   }
 };
 
+// One launch, or for float32 results several that add up Y.  The tensor core cuts
+// off what does not fit its accumulator at every MMA, always towards zero: over
+// K = 8192 a sum loses 4e-7 of its size, over 16384 1.1e-6 (a float32 sum in any
+// order 2e-7).  So no accumulator takes more than 8192 columns; the parts are added
+// in Y with rounding.
+constexpr int kSumBlocks = 8192 / kBK;
+
+template <typename Launch>
+cudaError_t in_parts(GemmArgs& a, int split, Launch launch) {
+  const int most = a.p.out == CSA_F32 ? kSumBlocks * split : a.kb_n;
+  const int all = a.kb_n;
+  cudaError_t e = cudaSuccess;
+  for (int at = 0; at < all && e == cudaSuccess; at += most) {
+    a.kb_first = at;
+    a.kb_n = all - at < most ? all - at : most;
+    a.add = at > 0;
+    e = launch(a);
+    if (e == cudaSuccess) ++*a.p.launches;
+  }
+  a.kb_n = all;
+  return e;
+}
+
 template <int OUT>
 cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   const Fp8GemmParams& p = a.p;
@@ -875,7 +915,9 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t pairs = sm_count() / 2;
   ClusterLaunch l(2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, smem, 2, stream);
-  return cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<OUT>, mx, mw, a);
+  return in_parts(a, 1, [&](const GemmArgs& part) {
+    return cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<OUT>, mx, mw, part);
+  });
 }
 
 template <int NT, int SPLIT, int OUT>
@@ -910,7 +952,7 @@ struct FewKernel {
     if (dev >= 0) known[dev].store(n, std::memory_order_relaxed);
     return n;
   }
-  static cudaError_t launch(const GemmArgs& a, cudaStream_t stream) {
+  static cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
     const Fp8GemmParams& p = a.p;
     CUtensorMap mx, mw;
     if (!make_map_u8_3d(&mx, p.x, (uint64_t)p.x_cols, (uint64_t)p.M, 1, kBK, NT) ||
@@ -919,7 +961,9 @@ struct FewKernel {
     const cudaError_t e = allow();
     if (e != cudaSuccess) return e;
     ClusterLaunch l(a.tiles * SPLIT, 128, smem, SPLIT, stream);
-    return cudaLaunchKernelEx(&l.cfg, fp8_gemm_few_kernel<NT, SPLIT, OUT>, mx, mw, a);
+    return in_parts(a, SPLIT, [&](const GemmArgs& part) {
+      return cudaLaunchKernelEx(&l.cfg, fp8_gemm_few_kernel<NT, SPLIT, OUT>, mx, mw, part);
+    });
   }
 };
 
