@@ -879,18 +879,22 @@ struct ClusterLaunch {
 // off what does not fit its accumulator at every MMA, always towards zero: over
 // K = 8192 a sum loses 4e-7 of its size, over 16384 1.1e-6 (a float32 sum in any
 // order 2e-7).  So no accumulator takes more than 8192 columns; the parts are added
-// in Y with rounding.
+// in Y with rounding.  The parts are of even length: a short last one would leave
+// shares of the few-row kernel without a chunk, and so without a sum.
 constexpr int kSumBlocks = 8192 / kBK;
+constexpr int kEven = kGroup * kChunk;   // parts start where scales load by the group
 
 template <typename Launch>
 cudaError_t in_parts(GemmArgs& a, int split, Launch launch) {
-  const int most = a.p.out == CSA_F32 ? kSumBlocks * split : a.kb_n;
-  const int all = a.kb_n;
+  const int all = a.kb_n, groups = (all + kEven - 1) / kEven;
+  const int parts =
+      a.p.out == CSA_F32 ? (all + kSumBlocks * split - 1) / (kSumBlocks * split) : 1;
   cudaError_t e = cudaSuccess;
-  for (int at = 0; at < all && e == cudaSuccess; at += most) {
-    a.kb_first = at;
-    a.kb_n = all - at < most ? all - at : most;
-    a.add = at > 0;
+  for (int i = 0; i < parts && e == cudaSuccess; ++i) {
+    const int end = (int)((int64_t)groups * (i + 1) / parts) * kEven;
+    a.kb_first = (int)((int64_t)groups * i / parts) * kEven;
+    a.kb_n = (end < all ? end : all) - a.kb_first;
+    a.add = i > 0;
     e = launch(a);
     if (e == cudaSuccess) ++*a.p.launches;
   }

@@ -265,7 +265,8 @@ def test_matmul_of_integers_is_exact(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(2048, 1536, 16992), (2048, 1531, 16384),
-                                   (700, 1000, 20000), (1700, 300, 24576), (40, 4000, 70000)])
+                                   (700, 1000, 20000), (1700, 300, 24576), (40, 4000, 70000),
+                                   (5, 1000, 65552), (100, 2000, 32784), (33, 300, 16400)])
 def test_matmul_long_float32_sums_are_added_in_parts(M, N, K):
     """float32 results of a K beyond 8192 a share are the rounded sums of the parts."""
     xc, xs, wc, ws = operands(M, N, K, 12)
