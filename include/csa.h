@@ -431,8 +431,8 @@ csa_status grouped_output_projection(int32_t dtype, int64_t T, int32_t H, int32_
  *   gain: [d] float32; sum_out: [T, d] (dtype), row stride sum_ld, or NULL; it
  *   may be x or residual itself (same pointer and stride).  Row strides in
  *   bytes are multiples of 16 and pointers 16-byte aligned.  The norm is taken
- *   of the unrounded h.  A row whose sum of squares is beyond float32 is
- *   scaled down first; a row with an infinity gives NaN there and 0 elsewhere,
+ *   of the unrounded h.  A row whose sum of squares is beyond float32, on
+ *   either side, is scaled first; a row with an infinity gives NaN there and 0 elsewhere,
  *   and an element whose h gain is beyond float32 gives NaN.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad dtype, T < 0, d < 1, a
  * stride below d, eps < 0 or NaN, sum_out without residual); CSA_E_UNSUPPORTED
@@ -445,7 +445,8 @@ csa_status rmsnorm_fp8(int32_t dtype, int64_t T, int32_t d, const void* x, int64
 /*
  * x [rows, d] (dtype, row stride ld elements) as FP8 activations
  * (block_rows = 1) or FP8 weights (block_rows = 128).  Errors: CSA_E_ARG (as
- * rmsnorm_fp8, or block_rows neither 1 nor 128), CSA_E_UNSUPPORTED.
+ * rmsnorm_fp8, or block_rows neither 1 nor 128), CSA_E_UNSUPPORTED (d not a
+ * multiple of 16, or above 2^30).
  */
 csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, int64_t ld,
                         int32_t block_rows, void* codes, void* scales, void* stream);
@@ -459,7 +460,7 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  *   y: [M, N], row stride y_ld elements (a column slice of a wider buffer is
  *   fine; any alignment of its element type).
  *   ws: >= csa_workspace_bytes(CSA_OP_FP8_MATMUL, ...) = 256 bytes (status
- *   word), zeroed before first use.
+ *   word), 16-byte aligned, zeroed before first use.
  * A row's result does not depend on the other rows' values; it may differ in
  * its last bits between values of M, which choose the split of K.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad out_dtype, negative M or

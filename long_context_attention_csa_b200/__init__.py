@@ -497,10 +497,10 @@ def _row_stride(t, shape, dtype, idx, what: str):
 
 
 def _cuda_rows(x, what: str):
-    """Device, shape and last dim (d > 0) of a CUDA tensor [..., d]."""
+    """Device, shape and last dim (0 < d < 2^31) of a CUDA tensor [..., d]."""
     idx, shape = x.get_device(), x.shape
-    if idx < 0 or len(shape) < 1 or shape[-1] < 1:
-        _refuse(f"{what}: a CUDA tensor [..., d]")
+    if idx < 0 or len(shape) < 1 or not 0 < shape[-1] < 1 << 31:
+        _refuse(f"{what}: a CUDA tensor [..., d], 0 < d < 2^31")
     return idx, shape, shape[-1]
 
 

@@ -399,7 +399,7 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
   if (dtype != CSA_F32 && dtype != CSA_BF16) return CSA_E_ARG;
   if (rows < 0 || d < 1 || (block_rows != 1 && block_rows != 128)) return CSA_E_ARG;
   if (!row_stride_ok(dtype, ld, d)) return CSA_E_ARG;
-  if (d % 16 != 0 || rows > 0x7fffffffLL) return CSA_E_UNSUPPORTED;
+  if (d % 16 != 0 || d > kFp8MaxDim || rows > 0x7fffffffLL) return CSA_E_UNSUPPORTED;
   if (rows == 0) return CSA_OK;
   if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes)) return CSA_E_ARG;
   g_launches.fetch_add(1);
@@ -418,7 +418,7 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
   if (!aligned16(x_codes) || !aligned16(w_codes) ||
       (reinterpret_cast<uintptr_t>(y) & (out_dtype == CSA_BF16 ? 1u : 3u)) != 0)
     return CSA_E_ARG;
-  if (!ws || ws_bytes < kWsScratch) return CSA_E_WORKSPACE;
+  if (!ws || !aligned16(ws) || ws_bytes < kWsScratch) return CSA_E_WORKSPACE;
   Fp8GemmParams p{};
   p.M = M;
   p.N = (int)N;

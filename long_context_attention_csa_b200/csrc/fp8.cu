@@ -318,10 +318,12 @@ __global__ void __launch_bounds__(512) rmsnorm_fp8_kernel(NormArgs a) {
     split(s, s0, s1);
     const float ms = row_sum(s0 + s1, it);
     float rstd = rsqrtf(fmaf(ms, n, a.eps));
-    // squares beyond float32 (|h| > 1e19): the same on 2^-80 h, where eps counts
-    // for nothing; a row that holds an infinity ends with 1/inf = 0
-    if (__any_sync(0xffffffffu, isinf(ms))) {   // alike in a row's warps
-      const float by = isinf(ms) ? 8.271806125530277e-25f : 1.f;   // 2^-80
+    // squares beyond float32 (|h| > 1e19), or near its smallest where eps does not
+    // hide them: the same on 2^-80 h or 2^80 h, eps times that twice; a row that
+    // holds an infinity ends with 1/inf = 0
+    const bool tiny = a.eps < 0x1p-100f && ms < 0x1p-100f;
+    if (__any_sync(0xffffffffu, isinf(ms) || tiny)) {   // alike in a row's warps
+      const float by = isinf(ms) ? 0x1p-80f : tiny ? 0x1p80f : 1.f;
       const f2 down = pair(by, by);
       f2 q = 0;
 #pragma unroll
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(512) rmsnorm_fp8_kernel(NormArgs a) {
       split(q, s0, s1);
       if (wpr > 1) __syncthreads();   // the slot has been read
       const float ms2 = row_sum(s0 + s1, it);
-      if (isinf(ms)) rstd = rsqrtf(ms2 * n);
+      if (by != 1.f) rstd = rsqrtf(fmaf(ms2, n, a.eps * by * by));
     }
     // y = h gain rstd: the largest |h gain| of a block, times rstd, gives its
     // scale, and one product per element, by rstd 2^-e, its code

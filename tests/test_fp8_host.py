@@ -49,7 +49,8 @@ def quant(L, dtype=BF16, rows=4, d=256, x=PTR, ld=256, br=1, codes=PTR, scales=P
     (dict(dtype=2), ARG), (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(br=0), ARG),
     (dict(br=64), ARG), (dict(x=None), ARG), (dict(x=MIS), ARG), (dict(codes=MIS), ARG),
     (dict(scales=None), ARG), (dict(ld=240), ARG), (dict(ld=257), ARG), (dict(d=250), UNSUPPORTED),
-    (dict(rows=1 << 31), UNSUPPORTED), (dict(rows=0), 0),
+    (dict(rows=1 << 31), UNSUPPORTED), (dict(d=(1 << 30) + 16, ld=(1 << 30) + 16), UNSUPPORTED),
+    (dict(rows=0), 0),
 ])
 def test_quantize_refusals(L, change, want):
     assert quant(L, **change) == want
@@ -68,7 +69,7 @@ def matmul(L, out=BF16, M=4, N=8, K=256, x=PTR, xs=PTR, w=PTR, ws_=PTR, y=PTR, l
     (dict(M=1 << 31), UNSUPPORTED), (dict(N=1 << 31, ld=1 << 31), UNSUPPORTED),
     (dict(K=(1 << 26) + 16), UNSUPPORTED),
     (dict(ws=None), WORKSPACE), (dict(ws_bytes=255), WORKSPACE),
-    (dict(M=0), 0), (dict(N=0, ld=0), 0),
+    (dict(ws=MIS), WORKSPACE), (dict(M=0), 0), (dict(N=0, ld=0), 0),
 ])
 def test_matmul_refusals(L, change, want):
     assert matmul(L, **change) == want

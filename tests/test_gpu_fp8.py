@@ -184,6 +184,22 @@ def test_rmsnorm_extremes():
     assert (c[2] == 0).all() and (exps(scales)[2] == -127).all()
 
 
+@pytest.mark.parametrize("d", [48, 640, 4096, 20480])
+def test_rmsnorm_of_rows_at_the_ends_of_float32(d):
+    """Squares that float32 does not hold, where eps does not hide them either."""
+    for eps in (0.0, float(np.float32(2.0 ** -133))):
+        x = normal((6, d), torch.float32, d)
+        for i, s in enumerate((2.0 ** -66, 2.0 ** -80, 2.0 ** -140, 2.0 ** 100, 1.0, 2.0 ** -50)):
+            x[i] *= s
+        g = 1 + 0.3 * normal((d,), torch.float32, 2)
+        for gain in (None, g):
+            codes, scales = csa.rmsnorm_fp8(x, None, gain, eps)
+            check_norm(x, None, gain, eps, codes, scales, eps)
+    x = normal((3, d), torch.float32, 1, 1e25)
+    codes, scales = csa.rmsnorm_fp8(x, eps=1e38)
+    check_norm(x, None, None, float(np.float32(1e38)), codes, scales)
+
+
 def test_rmsnorm_in_place_and_strided():
     x, r = normal((37, 512), torch.bfloat16, 8), normal((37, 512), torch.bfloat16, 9)
     want = csa.rmsnorm_fp8(x, r)
