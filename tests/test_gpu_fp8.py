@@ -307,6 +307,20 @@ def test_matmul_long_float32_sums_are_added_in_parts(M, N, K):
             assert torch.equal(a + b, y)
 
 
+def test_matmul_added_in_parts_replays():
+    """A captured call whose result is added up in Y starts over at every replay."""
+    xc, xs, wc, ws = operands(2048, 1536, 16384, 5)
+    room = csa.workspace(256)
+    want = csa.fp8_matmul(xc, xs, wc, ws, torch.float32, ws=room)
+    y = torch.full_like(want, float("nan"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa.fp8_matmul(xc, xs, wc, ws, y=y, ws=room)
+    for _ in range(3):
+        graph.replay()
+    assert torch.equal(y, want)
+
+
 def test_matmul_of_slices_of_a_batch():
     """Rows from the middle of a batch: scales that start anywhere."""
     xc, xs, wc, ws = operands(900, 300, 1168, 9)
