@@ -456,7 +456,7 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  * summed in float32 and rounded once to out_dtype (CSA_BF16 or CSA_F32).  The
  * tensor core's sums lose up to 2^-23 of their size every 32 columns; CSA_F32
  * results are therefore added up, in a fixed order, from sums over at most 8192
- * columns, each a launch of its own where K is longer.
+ * columns.
  *   y: [M, N], row stride y_ld elements (a column slice of a wider buffer is
  *   fine; any alignment of its element type).
  *   ws: >= csa_workspace_bytes(CSA_OP_FP8_MATMUL, ...) = 256 bytes (status

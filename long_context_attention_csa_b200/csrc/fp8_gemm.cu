@@ -23,6 +23,8 @@
 // in 9.3 (W's 33.6 MB take 5 us of it, at the copy rate).
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp8.h"
 #include "fp8_codes.cuh"
@@ -89,8 +91,9 @@ struct ScaleRows {
 
 struct GemmArgs {
   Fp8GemmParams p;
-  int kb_first, kb_n;    // scale blocks (stages) of K that this launch takes
-  bool add;              // onto what Y holds (float32)
+  int kb_first, kb_n;    // scale blocks (stages) of K that the launch takes (many rows: all)
+  int run;               // many rows, float32: blocks that one accumulator takes
+  bool add;              // few rows: onto what Y holds (float32)
   ScaleRows xs, ws;      // scales of X and of all W
   int w_rblocks;         // scale block rows of one W
   int y_align;           // 32, 16 or 1: the boundaries that rows of Y start on
@@ -138,9 +141,9 @@ __device__ __forceinline__ void store_words(void* dst, const uint32_t* w, bool s
 
 // Thirty-two consecutive values of one row that starts on a 16-byte boundary (32
 // with `sectors`), `n` of them inside Y.
-template <int OUT>
-__device__ __forceinline__ void store_row32(void* y, int64_t at, uint32_t* r, int n, bool sectors,
-                                            bool add) {
+template <int OUT, bool ADD>
+__device__ __forceinline__ void store_row32(void* y, int64_t at, uint32_t* r, int n,
+                                            bool sectors) {
   if constexpr (OUT == CSA_BF16) {
     bf16* dst = static_cast<bf16*>(y) + at;
     if (n >= 32) {
@@ -156,17 +159,24 @@ __device__ __forceinline__ void store_row32(void* y, int64_t at, uint32_t* r, in
     }
   } else {
     float* dst = static_cast<float*>(y) + at;
-    if (add) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < n) r[i] = __float_as_uint(dst[i] + __uint_as_float(r[i]));
-    }
     if (n >= 32) {
+      if constexpr (ADD) {
+        float4 q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = reinterpret_cast<const float4*>(dst)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          r[4 * i] = __float_as_uint(q[i].x + __uint_as_float(r[4 * i]));
+          r[4 * i + 1] = __float_as_uint(q[i].y + __uint_as_float(r[4 * i + 1]));
+          r[4 * i + 2] = __float_as_uint(q[i].z + __uint_as_float(r[4 * i + 2]));
+          r[4 * i + 3] = __float_as_uint(q[i].w + __uint_as_float(r[4 * i + 3]));
+        }
+      }
       store_words<32>(dst, r, sectors);
     } else {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (i < n) dst[i] = __uint_as_float(r[i]);
+        if (i < n) dst[i] = ADD ? dst[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
     }
   }
 }
@@ -220,10 +230,9 @@ __device__ __forceinline__ void store_rows32(E* dst, int64_t ld, const uint32_t*
   }
 }
 
-template <int OUT>
+template <int OUT, bool ADD>
 __device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, const uint32_t* r,
-                                             int rows, int n, bool add, uint32_t* stage,
-                                             int lane) {
+                                             int rows, int n, uint32_t* stage, int lane) {
   __syncwarp();
   if constexpr (OUT == CSA_BF16) {
 #pragma unroll
@@ -248,10 +257,21 @@ __device__ __forceinline__ void store_tile32(void* y, int64_t at, int64_t ld, co
       float* dst = static_cast<float*>(y) + at + half * ld + 16 * h + c;
       const uint32_t* src = stage + half * kStagePitch + c;
       const bool in = 16 * h + c < n;
+      if constexpr (ADD) {
+        float old[16];
 #pragma unroll
-      for (int q = 0; q < 32; q += 2, dst += 2 * ld) {
-        const float w = __uint_as_float(src[q * kStagePitch]);
-        if (in && q + half < rows) *dst = add ? *dst + w : w;
+        for (int q = 0; q < 16; ++q)
+          old[q] = in && 2 * q + half < rows ? dst[2 * q * ld] : 0.f;
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (in && 2 * q + half < rows)
+            dst[2 * q * ld] = old[q] + __uint_as_float(src[2 * q * kStagePitch]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 32; q += 2, dst += 2 * ld) {
+          const uint32_t w = src[q * kStagePitch];
+          if (in && q + half < rows) *dst = __uint_as_float(w);
+        }
       }
     }
   }
@@ -277,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const uint32_t first = blockIdx.x >> 1, step = gridDim.x >> 1, tiles = (uint32_t)a.tiles;
   const Fp8GemmParams& p = a.p;
+  const int run = OUT == CSA_F32 ? a.run : a.kb_n;   // a multiple of a group, or all
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -338,9 +359,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
           const uint32_t bar = cluster_addr(&full[s], 0);
           uint8_t* dst = sm + s * kStage;
-          const int k = (a.kb_first + kb) * kBK;
-          tma_load_3d_pair(dst, &map_x, bar, z * p.x_koff + k, (int32_t)m0, 0);
-          tma_load_3d_pair(dst + kTileA, &map_w, bar, k, n0 + (int)rank * (kN / 2), z);
+          tma_load_3d_pair(dst, &map_x, bar, z * p.x_koff + kb * kBK, (int32_t)m0, 0);
+          tma_load_3d_pair(dst + kTileA, &map_w, bar, kb * kBK,
+                           n0 + (int)rank * (kN / 2), z);
           ++it;
         }
       }
@@ -355,17 +376,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      uint32_t it = 0, ch = 0, gr = 0, n = 0;   // stages, chunks, groups, tiles
+      uint32_t it = 0, ch = 0, gr = 0, n = 0;   // stages, chunks, groups, sums
       bool landed = false;                      // stage `it` is known to have landed
-      for (uint32_t u = first; u < tiles; u += step, ++n) {
+      int kr = 0;                               // the sum's first block
+      for (uint32_t u = first; u < tiles; ++n) {
         if (*abort_flag || (n > 0 && !mbar_wait(tfree, (n - 1) & 1u))) {
           give_up(0x802u);
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + ((n & 1u) ? kAcc1 : 0u);
+        const int end = min(kr + run, a.kb_n);
         bool ok = true;
-        for (int kb = 0; kb < a.kb_n; ++kb, ++it) {
+        for (int kb = kr; kb < end; ++kb, ++it) {
           const uint32_t s = it % kStages, slot = gr % kSfSlots;
           const uint32_t sfa = tmem + kSfCol + (ch & 1u) * 12u, sfb = sfa + 4u;
           const int c = kb / kChunk % kGroup;   // chunk of its group
@@ -398,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kBK / 32; ++kk)
             mma_mxf8_ss_pair(d, smem_desc(sa + kk * 32, 16, 1024, 2),
                              smem_desc(sa + kTileA + kk * 32, 16, 1024, 2), idesc,
-                             sfa | (id << 30), sfb | (id << 30), (kb > 0 || kk > 0) ? 1u : 0u);
+                             sfa | (id << 30), sfb | (id << 30), (kb > kr || kk > 0) ? 1u : 0u);
           mma_commit_pair(&empty[s]);
-          const bool last = kb == a.kb_n - 1;
+          const bool last = kb == end - 1;
           if (kb % kChunk == kChunk - 1 || last) {
             mma_commit_one_of_pair(&cdone[ch & 1u]);
             ++ch;
@@ -412,6 +435,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         mma_commit_pair(tfull);
+        kr = end;
+        if (OUT != CSA_F32 || end == a.kb_n) {
+          kr = 0;
+          u += step;
+        }
       }
       mma_commit_one_of_pair(drain);
       mbar_wait(drain, 0);
@@ -428,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
-      const int xb0 = z * (p.x_koff / 128) + a.kb_first;
+      const int xb0 = z * (p.x_koff / 128);
       const int64_t wr = (int64_t)z * a.w_rblocks + n0 / 128;
       const bool second = n0 / 128 + 1 < a.w_rblocks;
       for (int kb = 0; kb < a.kb_n; kb += kGroup * kChunk, ++gr) {
@@ -439,8 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t m = m0 + 32 * i + lane;   // rows past the last: any row's scales
           a.xs.get<kGroup>(m < p.M ? m : p.M - 1, xb0 + kb, x[i]);
         }
-        a.ws.get<kGroup>(wr, a.kb_first + kb, w[0]);
-        a.ws.get<kGroup>(second ? wr + 1 : wr, a.kb_first + kb, w[1]);
+        a.ws.get<kGroup>(wr, kb, w[0]);
+        a.ws.get<kGroup>(second ? wr + 1 : wr, kb, w[1]);
         const uint32_t slot = gr % kSfSlots;
         ok = __all_sync(0xffffffffu, !*abort_flag && mbar_wait(&sempty[slot],
                                                                ((gr / kSfSlots) & 1u) ^ 1u));
@@ -474,10 +502,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_cluster_exec(free_bar);
     };
     uint32_t n = 0;
-    for (uint32_t u = first; u < tiles; u += step, ++n) {
+    int kr = 0;
+    for (uint32_t u = first; u < tiles; ++n) {
       int z, n0;
       int64_t m0;
       tile_of(u, z, m0, n0);
+      const bool add = OUT == CSA_F32 && kr > 0;
+      kr += run;
+      if (OUT != CSA_F32 || kr >= a.kb_n) {
+        kr = 0;
+        u += step;
+      }
       // warp-uniform decision: the TMEM loads below are warp-collective
       if (!__all_sync(0xffffffffu, !*abort_flag && mbar_wait(tfull, n & 1u))) {
         give_up(0x805u);
@@ -508,28 +543,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t mw = m0 + quarter * 32;   // this warp's first row
         const int rows = (int)(p.M - mw < 32 ? p.M - mw : 32);
         auto col = [&](int i) { return odd ? 32 * i : kN - 32 - 32 * i; };
-        auto store = [&](int cc, uint32_t* r) {
+        uint32_t r[2][32];
+        auto store = [&](int cc, uint32_t* r, auto adds) {
+          constexpr bool kAdd = decltype(adds)::value;
           const int n_in = p.N - n0 - cc;
           if (n_in <= 0) return;
           if (a.y_align < 16)
-            store_tile32<OUT>(p.y, at - lane * p.y_ld + cc, p.y_ld, r, rows, n_in, a.add,
-                              stage, lane);
+            store_tile32<OUT, kAdd>(p.y, at - lane * p.y_ld + cc, p.y_ld, r, rows, n_in, stage,
+                                    lane);
           else if (live)
-            store_row32<OUT>(p.y, at + cc, r, n_in, a.y_align >= 32, a.add);
+            store_row32<OUT, kAdd>(p.y, at + cc, r, n_in, a.y_align >= 32);
         };
-        uint32_t r[2][32];
+        auto store_all = [&](auto adds) {
+#pragma unroll 1
+          for (int i = 0; i < kN / 32; i += 2) {
+            tmem_ld32(base + col(i + 1), r[1]);
+            store(col(i), r[0], adds);
+            tmem_ld_wait();
+            if (i + 2 < kN / 32) tmem_ld32(base + col(i + 2), r[0]);
+            store(col(i + 1), r[1], adds);
+            tmem_ld_wait();
+          }
+        };
         tmem_ld32(base + col(0), r[0]);
         tmem_ld_wait();
         release();
-#pragma unroll 1
-        for (int i = 0; i < kN / 32; i += 2) {
-          tmem_ld32(base + col(i + 1), r[1]);
-          store(col(i), r[0]);
-          tmem_ld_wait();
-          if (i + 2 < kN / 32) tmem_ld32(base + col(i + 2), r[0]);
-          store(col(i + 1), r[1]);
-          tmem_ld_wait();
-        }
+        if (OUT == CSA_F32 && add) store_all(std::integral_constant<bool, OUT == CSA_F32>{});
+        else store_all(std::false_type{});
       }
     }
   }
@@ -758,6 +798,15 @@ __global__ void __launch_bounds__(128)
     uint32_t r[step];
     if constexpr (step == 32) tmem_ld32(base + t0, r);
     else tmem_ld16(base + t0, r);
+    if (OUT == CSA_F32 && !kSum && a.add) {
+      float old[step];
+#pragma unroll
+      for (int i = 0; i < step; ++i)
+        old[i] = inside && t0 + i < rows ? *reinterpret_cast<const float*>(dst + i * pitch) : 0.f;
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < step; ++i) r[i] = __float_as_uint(old[i] + __uint_as_float(r[i]));
+    }
     tmem_ld_wait();
 #pragma unroll
     for (int i = 0; i < step; ++i) {
@@ -770,7 +819,7 @@ __global__ void __launch_bounds__(128)
       } else if constexpr (!kRows) {
         if (inside && t < rows) {
           if (OUT == CSA_BF16) *reinterpret_cast<bf16*>(dst) = __float2bfloat16_rn(v);
-          else *reinterpret_cast<float*>(dst) = a.add ? *reinterpret_cast<float*>(dst) + v : v;
+          else *reinterpret_cast<float*>(dst) = v;
         }
         dst += pitch;
       }
@@ -800,8 +849,8 @@ __global__ void __launch_bounds__(128)
       const int64_t row = y0 + (int64_t)(k * SPLIT + rank) * p.y_ld;
       if constexpr (OUT == kFp8Out) {   // N, and rows of Y, are multiples of 128
         drop_infinities<4>(v);
-        const float am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),
-                                              fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));   // skips NaN
+        const float am = warp_max(fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])),   // skips NaN
+                                              fmaxf(fabsf(v[2]), fabsf(v[3]))), 0.f));
         const uint32_t byte = scale_byte(am);
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row + 4 * lane) =
             codes4(v, byte);
@@ -875,15 +924,18 @@ struct ClusterLaunch {
   }
 };
 
-// One launch, or for float32 results several that add up Y.  The tensor core cuts
-// off what does not fit its accumulator at every MMA, always towards zero: over
-// K = 8192 a sum loses 4e-7 of its size, over 16384 1.1e-6 (a float32 sum in any
-// order 2e-7).  So no accumulator takes more than 8192 columns; the parts are added
-// in Y with rounding.  The parts are of even length: a short last one would leave
-// shares of the few-row kernel without a chunk, and so without a sum.
+// The tensor core cuts off what does not fit its accumulator at every MMA, always
+// towards zero: over K = 8192 a sum loses 4e-7 of its size, over 16384 1.1e-6 (a
+// float32 sum in any order 2e-7).  So for float32 results no accumulator takes
+// more than 8192 columns, and the parts are added in Y with rounding: many rows
+// within a launch, a tile's sums one after the other (2048 x 2048 x 16384 55 us, a
+// launch a part 77, in bf16 46), few rows a launch a part, where K outgrows the
+// shares.
 constexpr int kSumBlocks = 8192 / kBK;
 constexpr int kEven = kGroup * kChunk;   // parts start where scales load by the group
 
+// One launch, or one a part.  The parts are of even length: a short last one would
+// leave shares without a chunk, and so without a sum.
 template <typename Launch>
 cudaError_t in_parts(GemmArgs& a, int split, Launch launch) {
   const int all = a.kb_n, groups = (all + kEven - 1) / kEven;
@@ -919,9 +971,10 @@ cudaError_t launch_many(GemmArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t pairs = sm_count() / 2;
   ClusterLaunch l(2 * (a.tiles < pairs ? a.tiles : pairs), kThreads, smem, 2, stream);
-  return in_parts(a, 1, [&](const GemmArgs& part) {
-    return cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<OUT>, mx, mw, part);
-  });
+  a.run = kSumBlocks;
+  e = cudaLaunchKernelEx(&l.cfg, fp8_gemm_kernel<OUT>, mx, mw, a);
+  if (e == cudaSuccess) ++*p.launches;
+  return e;
 }
 
 template <int NT, int SPLIT, int OUT>
@@ -1005,9 +1058,13 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   // The pairs' 256 x 256 tiles pay from about two thirds of a wave of K = 4096, or as
   // much work in more waves (measured, us, pairs against 128 x 128 tiles: 768 x 4096
   // x 4096 17.3, 17.7; 512 x 4096 x 4096 16.2, 14.4; 4096 x 2048 x 1024 13.4, 15.2;
-  // 2048 x 2048 x 2048 12.5, 11.3).
-  const int64_t pairs = tiles(2 * kTileM, kN);
-  if (p.M > 128 && pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536))
+  // 2048 x 2048 x 2048 12.5, 11.3).  Where the 128 x 128 tiles fit the SMs at once
+  // they use more of them (300 x 5000 x 8192 26.9, 22.3; 700 x 3000 x 16384 45.6,
+  // 43.4), unless a row of pairs takes a long K (256 x 8192 x 8192 24.9, 23.5; x 16384
+  // 43.4, 47.8) or Y are codes (a projection of 36 pairs, K = 8192: 42.0, 43.6).
+  const int64_t pairs = tiles(2 * kTileM, kN), t128 = tiles(128, kTileM);
+  const bool one_wave = OUT != kFp8Out && t128 <= sms && (p.M > 2 * kTileM || a.kb_n <= 64);
+  if (p.M > 128 && pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536) && !one_wave)
     return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
   // Smaller row tiles share the epilogue among more SMs, at the price of reading W
@@ -1018,7 +1075,7 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   // 4096: 13.8, 16.2); else 128 rows (96 x 4096 x 4096: 7.0, 64-row tiles 8.0).
   if (p.M <= 32 || (a.kb_n <= 8 && tiles(32, kTileM) <= sms))
     return launch_few<32, OUT>(a, stream);
-  const int64_t t128 = tiles(128, kTileM), t64 = tiles(64, kTileM);
+  const int64_t t64 = tiles(64, kTileM);
   if (p.M > 64 && OUT == kFp8Out) return launch_few<128, OUT>(a, stream);
   if (p.M <= 64 || t64 <= 32 || (a.kb_n <= 16 && t64 <= sms) ||
       (5 * t128 > 3 * sms && t128 <= sms && t64 <= 2 * sms))
