@@ -433,7 +433,7 @@ csa_status grouped_output_projection(int32_t dtype, int64_t T, int32_t H, int32_
  *   bytes are multiples of 16 and pointers 16-byte aligned.  The norm is taken
  *   of the unrounded h.  A row whose sum of squares is beyond float32, on
  *   either side, is scaled first; a row with an infinity gives NaN there and 0 elsewhere,
- *   and an element whose h gain is beyond float32 gives NaN.
+ *   and an element whose h gain, or whose y, is beyond float32 gives NaN.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad dtype, T < 0, d < 1, a
  * stride below d, eps < 0 or NaN, sum_out without residual); CSA_E_UNSUPPORTED
  * (d not a multiple of 16, or above 32768).

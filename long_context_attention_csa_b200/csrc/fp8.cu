@@ -362,9 +362,11 @@ __global__ void __launch_bounds__(512) rmsnorm_fp8_kernel(NormArgs a) {
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      byte[i] = scale_byte(fmaxf(top[i] * rstd, 0.f));
-      // rstd 2^-e stays finite for e >= -63; a block of zeros takes any factor
-      odd = odd || isinf(top[i]) || !(rstd < 1e18f) || (byte[i] < 64u && top[i] != 0.f);
+      const float most = top[i] * rstd;   // the block's largest |y|
+      byte[i] = scale_byte(fmaxf(most, 0.f));
+      // an infinite most: |h gain|, or y alone, is beyond float32; rstd 2^-e stays
+      // finite for e >= -63; a block of zeros takes any factor
+      odd = odd || !(most < INFINITY) || !(rstd < 1e18f) || (byte[i] < 64u && top[i] != 0.f);
       f[i] = rstd * pow2_of(254u - (byte[i] < 64u ? 64u : byte[i]));
     }
     if (__any_sync(0xffffffffu, odd)) {   // infinities, or values below 2^-54: step by step
