@@ -454,9 +454,10 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
 /*
  * y = x w^T of FP8 activations x [M, K] and FP8 weights w [N, K], products
  * summed in float32 and rounded once to out_dtype (CSA_BF16 or CSA_F32).  The
- * tensor core's sums lose up to 2^-23 of their size every 32 columns; CSA_F32
- * results are therefore added up, in a fixed order, from sums over at most 8192
- * columns.
+ * tensor core's sums lose up to 2^-23 of their size every 32 columns, always
+ * towards zero; CSA_F32 results are therefore added up, in a fixed order, from
+ * sums over at most 8192 columns.  CSA_BF16 results are one sum, of at most 2^17
+ * columns, which may lose 2^-11 of its size before it is rounded (2^-8).
  *   y: [M, N], row stride y_ld elements (a column slice of a wider buffer is
  *   fine; any alignment of its element type).
  *   ws: >= csa_workspace_bytes(CSA_OP_FP8_MATMUL, ...) = 256 bytes (status
@@ -465,7 +466,7 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  * its last bits between values of M, which choose the split of K.
  * Errors: CSA_E_ARG (null or misaligned pointers, bad out_dtype, negative M or
  * N, K < 1, y_ld < N), CSA_E_UNSUPPORTED (K not a multiple of 16, M or N
- * beyond 2^30, K beyond 2^26), CSA_E_WORKSPACE.
+ * beyond 2^30, K beyond 2^26 or, to CSA_BF16, beyond 2^17), CSA_E_WORKSPACE.
  */
 csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const void* x_codes,
                       const void* x_scales, const void* w_codes, const void* w_scales, void* y,
@@ -481,8 +482,9 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
  * [T, d] bf16.  ws: >= csa_workspace_bytes(CSA_OP_OUT_PROJ_FP8, dtype, 1, T,
  * H, c, g d_g, 0, 0); it holds the codes of o and v during the call, so calls
  * that overlap on the GPU need one each.
- * Errors: CSA_E_ARG, CSA_E_WORKSPACE, and CSA_E_UNSUPPORTED unless H % g == 0
- * and (H/g) c and d_g are multiples of 128.
+ * Errors: CSA_E_ARG, CSA_E_WORKSPACE, and CSA_E_UNSUPPORTED unless H % g == 0,
+ * (H/g) c and d_g are multiples of 128, and (H/g) c and g d_g, the columns that
+ * one sum takes (see fp8_matmul), are at most 2^17.
  */
 csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, int32_t c,
                                          int32_t g, int32_t d_g, int32_t d, const void* o,

@@ -589,8 +589,8 @@ def fp8_matmul(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16, y
                stream=None):
     """y = x w^T of FP8 activations (codes [..., K], scales [..., ceil(K/128)])
     and FP8 weights (codes [N, K], scales [ceil(N/128), ceil(K/128)]) -> [..., N]
-    bf16 or fp32.  ``y``, whose dtype then counts, may be a two-dimensional
-    column slice of a wider buffer."""
+    bf16 (K <= 2^17) or fp32.  ``y``, whose dtype then counts, may be a
+    two-dimensional column slice of a wider buffer."""
     if stream is not None:
         return _on(stream, x_codes, fp8_matmul, x_codes, x_scales, w_codes, w_scales, out_dtype, y,
                    ws)

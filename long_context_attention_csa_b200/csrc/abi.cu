@@ -412,7 +412,9 @@ csa_status fp8_matmul(int32_t out_dtype, int64_t M, int64_t N, int64_t K, const 
                       int64_t y_ld, void* ws, size_t ws_bytes, void* stream) {
   if (out_dtype != CSA_F32 && out_dtype != CSA_BF16) return CSA_E_ARG;
   if (M < 0 || N < 0 || K < 1 || y_ld < N) return CSA_E_ARG;
-  if (K % 16 != 0 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxK) return CSA_E_UNSUPPORTED;
+  if (K % 16 != 0 || M > kFp8MaxDim || N > kFp8MaxDim ||
+      K > (out_dtype == CSA_F32 ? kFp8MaxK : kFp8MaxOneSum))
+    return CSA_E_UNSUPPORTED;
   if (M == 0 || N == 0) return CSA_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return CSA_E_ARG;
   if (!aligned16(x_codes) || !aligned16(w_codes) ||
@@ -454,7 +456,8 @@ csa_status grouped_output_projection_fp8(int32_t dtype, int64_t T, int32_t H, in
   if (T < 0 || H <= 0 || c <= 0 || g <= 0 || d_g <= 0 || d <= 0) return CSA_E_ARG;
   const int64_t hc = (int64_t)H * c, gd = (int64_t)g * d_g;
   if (H % g != 0 || (hc / g) % 128 != 0 || d_g % 128 != 0) return CSA_E_UNSUPPORTED;
-  if (T > kFp8MaxDim || hc > kFp8MaxK || gd > kFp8MaxK || d > kFp8MaxDim || g > 65535)
+  if (T > kFp8MaxDim || hc > kFp8MaxK || hc / g > kFp8MaxOneSum || gd > kFp8MaxOneSum ||
+      d > kFp8MaxDim || g > 65535)
     return CSA_E_UNSUPPORTED;
   if (T == 0) return CSA_OK;
   if (!o || !w_group || !w_group_scales || !w_out || !w_out_scales || !y) return CSA_E_ARG;

@@ -13,6 +13,12 @@ constexpr int kFp8MaxNormDim = 32768;   // columns rmsnorm_fp8 holds in register
 
 constexpr int64_t kFp8MaxDim = 1 << 30;  // rows and columns of a product: tile ends fit 32 bits
 constexpr int64_t kFp8MaxK = 1 << 26;    // a tile's sum ends well within a bounded wait
+// Columns of one tensor-core sum.  Each MMA cuts off up to 2^-23 of the sum so far,
+// every 32 columns: at most 2^-11 over 2^17 columns, an eighth of bf16's half step
+// (operands of one sign, 2^17 columns: 1.6e-4).  bf16 and E4M3 results, which no
+// float32 buffer adds up from parts, take no more; over 2^20 columns the cut would
+// reach bf16's rounding itself.
+constexpr int64_t kFp8MaxOneSum = 1 << 17;
 
 struct NormParams {
   int64_t T;

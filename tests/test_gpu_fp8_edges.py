@@ -1,11 +1,17 @@
-"""The 8-bit projection path at its edges: results beyond float32."""
+"""The 8-bit projection path at its edges: results beyond float32, sums of one sign.
+
+Sums of one sign.  The tensor core adds 32 products a step and cuts its sum off
+towards zero, by one unit in the last place (2^-23 of the sum so far) at most.  Where
+all products have one sign nothing cancels: the cuts of K columns add up to
+K/32 2^-23 of the result at most, and as the sum grows evenly to half of that.
+"""
 import numpy as np
 import pytest
 import torch
 
 import oracle
 from parity import f64
-from test_gpu_fp8 import D_NORM, exps
+from test_gpu_fp8 import D_NORM, exps, values
 import long_context_attention_csa_b200 as csa
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +47,35 @@ def test_rmsnorm_results_beyond_float32_are_nan(d, wide, dtype):
     r = np.abs(np.ldexp(y, -oracle._fp8_spread(e, 1, y.shape)))[~over]
     half = np.ldexp(1.0, np.maximum(np.frexp(r * (1 + D_NORM))[1] - 1, -6) - 4)
     assert (np.abs(np.abs(got[~over]) - r) <= half + D_NORM * r).all()
+
+
+# ---- fp8_matmul ----------------------------------------------------------------------
+
+def one_signed(M, N, K, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn((M, K), generator=gen, device=DEV).abs_()
+    out = csa.fp8_quantize(x)
+    del x
+    return (*out, *csa.fp8_quantize(torch.randn((N, K), generator=gen, device=DEV).abs_(), 128))
+
+
+def exact_product(xc, xs, wc, ws, step=8192):
+    """x w^T in float64 on the device, `step` columns (a multiple of 128) at a time."""
+    K, y = xc.shape[1], 0.0
+    for k in range(0, K, step):
+        e = min(K, k + step)
+        x, w = (values(c.view(torch.uint8)[:, k:e].contiguous().view(torch.float8_e4m3fn),
+                       s.view(torch.uint8)[:, k // 128:-(-e // 128)], rows)
+                for c, s, rows in ((xc, xs, 1), (wc, ws, 128)))
+        y = y + x @ w.t()
+    return y
+
+
+@pytest.mark.parametrize("M,N", [(1, 256), (40, 300), (2048, 1024)])
+def test_matmul_longest_bf16_sum_of_one_sign(M, N):
+    """A bf16 result's one sum at the longest K: the cut is an eighth of the rounding."""
+    K = 1 << 17
+    ops = one_signed(M, N, K, M)
+    ref = exact_product(*ops)
+    d = (csa.fp8_matmul(*ops).double() - ref).abs()
+    assert bool((d <= (2.0 ** -8 * (1 + 2.0 ** -11) + K / 32 * 2.0 ** -23) * ref).all())
