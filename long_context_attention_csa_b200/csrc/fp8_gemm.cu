@@ -925,12 +925,15 @@ struct ClusterLaunch {
 };
 
 // The tensor core cuts off what does not fit its accumulator at every MMA, always
-// towards zero: over K = 8192 a sum loses 4e-7 of its size, over 16384 1.1e-6 (a
-// float32 sum in any order 2e-7).  So for float32 results no accumulator takes
-// more than 8192 columns, and the parts are added in Y with rounding: many rows
-// within a launch, a tile's sums one after the other (2048 x 2048 x 16384 55 us, a
-// launch a part 77, in bf16 46), few rows a launch a part, where K outgrows the
-// shares.
+// towards zero.  Relative to the result, 2048 x 1024 x K, operands of mean zero /
+// of one sign (whose cuts all add up): K = 8192 4.9e-7 / 3.9e-6, 16384 1.2e-6 /
+// 9.9e-6, 65536 7.7e-6 / 6.0e-5; a float32 product of the same K = 8192 operands on
+// the CUDA cores 1.3e-7 / 4.3e-7.  So for float32 results no accumulator takes more
+// than 8192 columns, and the parts are added in Y with rounding: many rows within a
+// launch, a tile's sums one after the other (2048 x 2048 x 16384 55 us, a launch a
+// part 77, in bf16 46), few rows a launch a part, where K outgrows the shares.
+// Parts of 4096 columns would halve the cut and take a quarter longer (8192 x 4096 x
+// 8192: 201 us, 254; of 2048, 372).
 constexpr int kSumBlocks = 8192 / kBK;
 constexpr int kEven = kGroup * kChunk;   // parts start where scales load by the group
 

@@ -79,3 +79,17 @@ def test_matmul_longest_bf16_sum_of_one_sign(M, N):
     ref = exact_product(*ops)
     d = (csa.fp8_matmul(*ops).double() - ref).abs()
     assert bool((d <= (2.0 ** -8 * (1 + 2.0 ** -11) + K / 32 * 2.0 ** -23) * ref).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 300, 1 << 20), (100, 10240, 1 << 16), (2048, 1536, 1 << 16)])
+def test_matmul_float32_sums_of_one_sign_are_added_in_parts(M, N, K):
+    """Each part's cut is at most half of 8192/32 2^-23 (and a sixteenth, as products are
+    not all alike), a rounding for every part and share comes on top.  One sum of all
+    columns that a share takes here (2^16 or 2^17) loses twice to four times that."""
+    ops = one_signed(M, N, K, M)
+    ref = exact_product(*ops)
+    n0 = csa.csa_launch_count()
+    y = csa.fp8_matmul(*ops, out_dtype=torch.float32).double()
+    assert M > 128 or csa.csa_launch_count() - n0 > 1      # few rows: a launch a part
+    rel = float(((y - ref).abs() / ref).max())
+    assert rel <= 17 / 16 * 128 * 2.0 ** -23 + (K / 8192 + 8) * 2.0 ** -24, rel
