@@ -24,3 +24,22 @@ def test_matmul_columns_of_one_sum(L, out, K, want):
 ])
 def test_projection_columns_of_one_sum(L, change, want):
     assert proj(L, ws=None, **change) == want
+
+
+def test_a_large_workspace_of_the_calls_own_is_zeroed_at_its_status_word_only(monkeypatch):
+    import torch
+
+    import long_context_attention_csa_b200 as csa
+
+    asked = []
+
+    def workspace(nbytes, device=None):
+        asked.append(nbytes)
+        return torch.zeros(max(nbytes, 256), dtype=torch.uint8)
+
+    monkeypatch.setattr(csa, "workspace", workspace)
+    for n in (256, 4096, 16 << 20, (16 << 20) + 256, 64 << 20):
+        address, size, ws = csa._ws(None, n, 0)
+        assert address == ws.data_ptr() and size == ws.numel() >= n
+        assert int(ws[:256].max()) == 0
+    assert max(asked) <= 16 << 20

@@ -11,7 +11,7 @@ import torch
 
 import oracle
 from parity import f64
-from test_gpu_fp8 import D_NORM, exps, values
+from test_gpu_fp8 import D_NORM, exps, proj_inputs, values
 import long_context_attention_csa_b200 as csa
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +93,22 @@ def test_matmul_float32_sums_of_one_sign_are_added_in_parts(M, N, K):
     assert M > 128 or csa.csa_launch_count() - n0 > 1      # few rows: a launch a part
     rel = float(((y - ref).abs() / ref).max())
     assert rel <= 17 / 16 * 128 * 2.0 ** -23 + (K / 8192 + 8) * 2.0 ** -24, rel
+
+
+# ---- grouped_output_projection_fp8 ----------------------------------------------------
+
+def test_projection_with_a_large_workspace_of_its_own_captured():
+    """The call's own workspace, of which only the status word is zeroed, inside a graph
+    that is replayed on other inputs."""
+    x = proj_inputs(2000, 32, 512, 4, 256, 640, 1)      # 33 MB of codes
+    y = torch.empty(2000, 640, dtype=torch.bfloat16, device=DEV)
+    csa.grouped_output_projection_fp8(*x, y=y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        csa.grouped_output_projection_fp8(*x, y=y)
+    for seed in (2, 3):
+        x[0].copy_(proj_inputs(2000, 32, 512, 4, 256, 640, seed)[0])
+        graph.replay()
+        ws = csa.workspace(csa.csa_workspace_bytes(csa.CSA_OP_OUT_PROJ_FP8, torch.bfloat16, 1,
+                                                   2000, 32, 512, 1024))
+        assert torch.equal(y, csa.grouped_output_projection_fp8(*x, ws=ws))
