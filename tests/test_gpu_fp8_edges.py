@@ -11,7 +11,7 @@ import torch
 
 import oracle
 from parity import f64
-from test_gpu_fp8 import D_NORM, exps, proj_inputs, values
+from test_gpu_fp8 import D_NORM, bits, check_norm, exps, normal, proj_inputs, values
 import long_context_attention_csa_b200 as csa
 
 pytestmark = pytest.mark.gpu
@@ -47,6 +47,35 @@ def test_rmsnorm_results_beyond_float32_are_nan(d, wide, dtype):
     r = np.abs(np.ldexp(y, -oracle._fp8_spread(e, 1, y.shape)))[~over]
     half = np.ldexp(1.0, np.maximum(np.frexp(r * (1 + D_NORM))[1] - 1, -6) - 4)
     assert (np.abs(np.abs(got[~over]) - r) <= half + D_NORM * r).all()
+
+
+@pytest.mark.parametrize("T,d,dtype,residual", [
+    (40000, 48, torch.bfloat16, False), (20000, 128, torch.bfloat16, True),   # rows of part of a warp
+    (20000, 128, torch.float32, False), (12000, 256, torch.float32, True),
+    (6000, 512, torch.bfloat16, True), (6000, 528, torch.bfloat16, False), (4000, 1040, torch.float32, True),
+    (15000, 4096, torch.bfloat16, True), (15000, 2048, torch.float32, True),  # the short walks
+    (15000, 4096, torch.bfloat16, False),
+    (400, 16384, torch.float32, True), (400, 16384, torch.float32, False),    # no loads ahead
+    (400, 32768, torch.bfloat16, True), (400, 32768, torch.float32, True),
+])
+def test_rmsnorm_of_more_rows_than_run_at_once(T, d, dtype, residual):
+    """Blocks that walk several rows: every row equals, bit for bit, the same row in a
+    batch so small that each block takes one, and sampled rows are right."""
+    x = normal((T, d), dtype, T + d)
+    res = normal((T, d), dtype, T + d + 1, 3.0) if residual else None
+    gain = 1 + 0.3 * normal((d,), torch.float32, 2)
+    whole = csa.rmsnorm_fp8(x, res, gain)
+    piece = 100 if d >= 512 else 1000
+    for a in range(0, T, piece):
+        r = slice(a, min(T, a + piece))
+        part = csa.rmsnorm_fp8(x[r], None if res is None else res[r], gain)
+        for p, q in zip(part, whole):
+            assert torch.equal(bits(p), bits(q[r])), a
+    rows = [0, 1, T // 2, T - 2, T - 1]
+    check_norm(x[rows], None if res is None else res[rows], gain, 1e-6, whole[0][rows],
+               bits(whole[1])[rows])
+    if residual:
+        assert torch.equal(whole[2], (x.float() + res.float()).to(dtype))
 
 
 # ---- fp8_matmul ----------------------------------------------------------------------
