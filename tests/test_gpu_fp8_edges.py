@@ -124,6 +124,23 @@ def test_matmul_float32_sums_of_one_sign_are_added_in_parts(M, N, K):
     assert rel <= 17 / 16 * 128 * 2.0 ** -23 + (K / 8192 + 8) * 2.0 ** -24, rel
 
 
+@pytest.mark.parametrize("M,N,K", [
+    (1, 640, 1 << 16), (3, 2000, 8192), (32, 300, 1 << 16), (100, 1000, 40000), (300, 520, 16384),
+    (777, 1111, 1040), (2048, 1536, 16384), (2049, 2300, 8192),
+])
+def test_matmul_of_one_signed_integers_is_exact(M, N, K):
+    """Whole numbers from 0 to 15, whose sums grow to 22 bits and stay below 2^24 at any
+    K up to 2^16: a product that held fewer bits, or lost a column, would differ.  bf16
+    results are the exact sums rounded once."""
+    gen = torch.Generator(device=DEV).manual_seed(M + N + K)
+    xc, xs = csa.fp8_quantize(torch.randint(0, 16, (M, K), generator=gen, device=DEV).float())
+    wc, ws = csa.fp8_quantize(torch.randint(0, 16, (N, K), generator=gen, device=DEV).float(), 128)
+    ref = exact_product(xc, xs, wc, ws)
+    assert float(ref.max()) < 2 ** 24
+    assert torch.equal(csa.fp8_matmul(xc, xs, wc, ws, out_dtype=torch.float32).double(), ref)
+    assert torch.equal(csa.fp8_matmul(xc, xs, wc, ws), ref.float().bfloat16())
+
+
 # ---- grouped_output_projection_fp8 ----------------------------------------------------
 
 def test_projection_with_a_large_workspace_of_its_own_captured():
