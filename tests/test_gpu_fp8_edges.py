@@ -158,3 +158,50 @@ def test_projection_with_a_large_workspace_of_its_own_captured():
         ws = csa.workspace(csa.csa_workspace_bytes(csa.CSA_OP_OUT_PROJ_FP8, torch.bfloat16, 1,
                                                    2000, 32, 512, 1024))
         assert torch.equal(y, csa.grouped_output_projection_fp8(*x, ws=ws))
+
+
+def integer_weights(rows, cols, gen, top):
+    """FP8 weights that are whole numbers from -top to top (at most 15: E4M3 holds them)."""
+    return csa.fp8_quantize(torch.randint(-top, top + 1, (rows, cols), generator=gen,
+                                          device=DEV).float(), 128)
+
+
+@pytest.mark.parametrize("T,H,c,g,dg", [
+    (4100, 32, 128, 4, 384),     # many rows: a last tile of 4 rows, half a tile past d_g
+    (4100, 32, 128, 4, 640), (3100, 64, 256, 4, 128), (2048, 32, 128, 8, 1024),
+    (300, 32, 128, 4, 384), (33, 8, 256, 2, 256), (1, 8, 256, 2, 128),   # few rows
+])
+def test_projection_intermediate_is_exact_on_integers(T, H, c, g, dg):
+    """Whole numbers up to 15 and 7 in o and w_group: the grouped product's sums (below 2^24)
+    are exact, and so are their codes; w_out is the unit matrix, whose product is the
+    intermediate itself, in bf16 without a rounding.  A row that holds an infinity, and
+    one whose sums are beyond float32, are NaN and leave the others alone."""
+    gen = torch.Generator(device=DEV).manual_seed(T + dg)
+    kg, gd = H // g * c, g * dg
+    o = torch.randint(-15, 16, (T, H, c), generator=gen, device=DEV).bfloat16()
+    wg, wgs = integer_weights(gd, kg, gen, 7)
+    wo, wos = csa.fp8_quantize(torch.eye(gd, device=DEV), 128)
+    bad = [T // 2, T - 1] if T > 2 else []
+    if bad:
+        o[bad[0], H // 2, 3] = float("inf")
+        # codes and weights are finite, their sum is not: 2^127 a column, of the sign of
+        # the first weight row's
+        o[bad[1], :H // g] = torch.copysign(torch.tensor(2.0 ** 127, device=DEV),
+                                            wg[0].float()).view(H // g, c).bfloat16()
+    y = csa.grouped_output_projection_fp8(o, wg.view(g, dg, kg),
+                                          wgs.view(g, dg // 128, kg // 128), wo, wos)
+    assert bool(torch.isnan(y[bad]).all())
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    w = values(wg, wgs, 128).view(g, dg, kg)
+    v = torch.einsum("tgk,gnk->tgn", o[keep].double().view(-1, g, kg), w).reshape(-1, gd)
+    assert float(v.abs().max()) < 2 ** 24
+    assert np.array_equal(f64(y[keep]), oracle.fp8_values(*oracle.fp8_quantize(f64(v))))
+
+
+@pytest.mark.parametrize("T", [5, 700, 3000])
+def test_projection_repeats_itself(T):
+    x = proj_inputs(T, 32, 128, 4, 512, 520, T)
+    y = csa.grouped_output_projection_fp8(*x)
+    for _ in range(3):
+        assert torch.equal(csa.grouped_output_projection_fp8(*x), y)
