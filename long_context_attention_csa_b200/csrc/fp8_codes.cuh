@@ -36,8 +36,4 @@ __device__ __forceinline__ uint32_t codes4(const float* v, uint32_t byte) {
           << 16);
 }
 
-__device__ __forceinline__ uint2 codes8(const float* v, uint32_t byte) {
-  return make_uint2(codes4(v, byte), codes4(v + 4, byte));
-}
-
 }  // namespace csa

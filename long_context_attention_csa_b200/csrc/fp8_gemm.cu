@@ -994,8 +994,8 @@ struct FewKernel {
   // answer is for one CTA on an SM (74, 33 and 15 clusters of two, four and eight);
   // with two, odd SMs of a GPC pair up, which makes two more (32 x N x 4096 by
   // fours: 68 tiles 9.9 us, 72 14.3; by eights: 32 tiles 10.1, 34 14.3).
-  static constexpr int per_sm = 2 * (smem + 1024) <= 233472 ? 2 : 1;
   static int clusters() {
+    constexpr int per_sm = 2 * (smem + 1024) <= 233472 ? 2 : 1;
     static std::atomic<int> known[kMaxDevices];
     const int dev = current_device();
     int n = dev >= 0 ? known[dev].load(std::memory_order_relaxed) : 0;
