@@ -16,11 +16,11 @@
 //
 // Two kernels.  fp8_gemm_kernel: many rows, X rows on the MMA's M, 256 columns
 // on N, persistent.  Bound by the tensor cores and, back to back, by the chip's
-// power: 8192 x 8192 x 4096 to bf16 in 190 us alone (2.9 PFLOP/s), 216-223 us back
-// to back (2.5 PFLOP/s at 1.3 GHz).
+// power: 8192 x 8192 x 4096 to bf16 in 190 us alone (2.9 PFLOP/s), back to back in
+// 215 to 231, by the card (2.4 to 2.5 PFLOP/s at 1.3 GHz).
 // fp8_gemm_few_kernel: few rows, where the bytes of W are the bound: W rows on M,
-// the few X rows on N, K split over a cluster.  1 x 8192 x 4096 in 8.4 us, 32 rows
-// in 9.3 (W's 33.6 MB take 5 us of it, at the copy rate).
+// the few X rows on N, K split over a cluster.  1 x 8192 x 4096 in 8.5 us, 32 rows
+// in 9.5 (W's 33.6 MB take 5 us of it, at the copy rate).
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -1058,24 +1058,34 @@ cudaError_t launch(GemmArgs& a, cudaStream_t stream) {
   auto tiles = [&](int64_t rows, int64_t cols) {
     return (int64_t)p.Z * ((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols);
   };
-  // The pairs' 256 x 256 tiles pay from about two thirds of a wave of K = 4096, or as
-  // much work in more waves (measured, us, pairs against 128 x 128 tiles: 768 x 4096
-  // x 4096 17.3, 17.7; 512 x 4096 x 4096 16.2, 14.4; 4096 x 2048 x 1024 13.4, 15.2;
-  // 2048 x 2048 x 2048 12.5, 11.3).  Where the 128 x 128 tiles fit the SMs at once
-  // they use more of them (300 x 5000 x 8192 26.9, 22.3; 700 x 3000 x 16384 45.6,
-  // 43.4), unless a row of pairs takes a long K (256 x 8192 x 8192 24.9, 23.5; x 16384
-  // 43.4, 47.8) or Y are codes (a projection of 36 pairs, K = 8192: 42.0, 43.6).
+  // Many rows: the pairs' 256 x 256 tiles pay from about two thirds of a wave of K =
+  // 4096, or as much work in more waves.  Us between captured launches, the pairs /
+  // 128-row / 64-row tiles of the few-row kernel (128 columns each):
+  //    768 x 4096 x 4096   20.7 / 21.3 / 28.4
+  //   4096 x 2048 x 1024   14.2 / 16.1 / 23.6
+  //   2048 x 2048 x 2048   13.4 / 12.3 / 18.3
+  //    512 x 4096 x 4096   16.0 / 15.5 / 13.8
+  // Where 128 x 128 tiles would fit the SMs at once the few-row kernel, which then
+  // takes 64 rows, uses more of them,
+  //    300 x 5000 x 8192   27.1 / 27.1 / 23.4
+  //    512 x 4096 x 8192   27.5 / 29.4 / 23.7
+  //    700 x 3000 x 16384  46.1 / 51.5 / 45.6
+  //    256 x 8192 x 8192   27.2 / 30.7 / 26.4
+  // unless one row of pairs takes a longer K,
+  //    256 x 8192 x 16384  45.3 / 55.8 / 50.3
+  // or Y are codes (a projection of 36 pairs, K = 8192: pairs 42.0, few 43.6).
   const int64_t pairs = tiles(2 * kTileM, kN), t128 = tiles(128, kTileM);
   const bool one_wave = OUT != kFp8Out && t128 <= sms && (p.M > 2 * kTileM || a.kb_n <= 64);
   if (p.M > 128 && pairs >= 32 && pairs * a.kb_n >= (2 * pairs > sms ? 1024 : 1536) && !one_wave)
     return launch_many<OUT>(a, stream);
   if (p.M <= 16) return launch_few<16, OUT>(a, stream);
-  // Smaller row tiles share the epilogue among more SMs, at the price of reading W
-  // again: 32 rows where K <= 1024 and the tiles fit the SMs at once (100 x 256 x
-  // 640: 4.4 us, 128-row tiles 6.5), 64 rows where K <= 2048 and they do (777 x
-  // 1111 x 1040: 6.2, 7.9), where there are few at any K (300 x 300 x 8192: 5.9,
-  // 6.8), and where 128-row tiles leave SMs idle that these fill (512 x 4096 x
-  // 4096: 13.8, 16.2); else 128 rows (96 x 4096 x 4096: 7.0, 64-row tiles 8.0).
+  // Few rows, smaller row tiles: more SMs share the epilogue, at the price of reading
+  // W again.  32 rows where K <= 1024 and the tiles fit the SMs at once (100 x 256 x
+  // 640: 4.4 us, 128-row tiles 6.5); 64 rows where K <= 2048 and they do (777 x 1111 x
+  // 1040: 5.9, 7.9), where there are few at any K (300 x 300 x 8192: 6.0, 7.3), and
+  // where 128-row tiles would run one to an SM on 60% of the SMs or more: the 64-row
+  // ones run two, with twice the stages in flight (512 x 4096 x 4096: 13.8, 15.5).
+  // Else 128 rows (96 x 4096 x 4096: 8.7, 64-row tiles 9.1).
   if (p.M <= 32 || (a.kb_n <= 8 && tiles(32, kTileM) <= sms))
     return launch_few<32, OUT>(a, stream);
   const int64_t t64 = tiles(64, kTileM);
