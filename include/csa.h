@@ -457,8 +457,9 @@ csa_status fp8_quantize(int32_t dtype, int64_t rows, int32_t d, const void* x, i
  * tensor core's sums lose up to 2^-23 of their size every 32 columns, always
  * towards zero; CSA_F32 results are therefore added up, in a fixed order, from
  * sums over at most 8192 columns (at that length 5e-7 of a result whose products
- * have both signs was seen lost, 4e-6 where they have one).  CSA_BF16 results are one sum, of at most 2^17
- * columns, which may lose 2^-11 of its size before it is rounded (2^-8).
+ * have both signs was seen lost, 4e-6 where they have one).  CSA_BF16 results are
+ * one sum, of at most 2^17 columns, which may lose 2^-11 of its size before it is
+ * rounded (2^-8); longer products go to CSA_F32.
  *   y: [M, N], row stride y_ld elements (a column slice of a wider buffer is
  *   fine; any alignment of its element type).
  *   ws: >= csa_workspace_bytes(CSA_OP_FP8_MATMUL, ...) = 256 bytes (status
